@@ -332,6 +332,122 @@ TLS_API tls_status tls_prefetch_diff(const tls_shape *s, int32_t n_slots, const 
                              int32_t *slot_of_block, int32_t *block_of_slot, const int32_t *prev_block_idx,
                              const int32_t *next_block_idx, int32_t *n_new_out, int32_t *jobs_ws, void *stream);
 
+/* ---- 4-bit KV cache ---------------------------------------------------------
+ * A cache of K and V in 4 bits (no counterpart in the paper: an addition of
+ * this library), 144 bytes per token and KV head at d 128 where bf16 takes 512.
+ * One record per (sequence, KV head, token), 9 d / 8 bytes:
+ *   [K codes d/2][K scales d/16][V scales d/16][V codes d/2]
+ * code: e2m1 (sign, 2 exponent bits, 1 mantissa bit: 0 .5 1 1.5 2 3 4 6),
+ *   channel 2i in the low nibble of byte i;
+ * scale: one byte b per 16 channels, the fp16 number with the bits b << 7.
+ *   A group's scale is max|x| / 6 and a code x / scale, both rounded to nearest
+ *   even (scale 0: codes 0).  A group that holds an infinity or a NaN gets the
+ *   scale byte 0xff and reads back as NaN.  Magnitudes above 61440 are clamped.
+ * Shapes: GQA (v_is_k_prefix 0) with kv_dtype BF16 (the type of q and of the
+ * rows that go in or come out); others return TLS_ERR_UNSUPPORTED.  cache:
+ * device [B][H_kv][max_ctx][9 d / 8] bytes, 16-byte aligned.  The selection
+ * stages run as before, on the summary and slab that tls_kv4_append keeps. */
+
+/* Bytes of the 4-bit cache; 0 for an invalid shape (see tls_last_error). */
+TLS_API size_t tls_kv4_cache_bytes(const tls_shape *s);
+
+/* Bytes of device workspace for tls_kv4_attn_decode (partials that only calls
+ * with few groups use; at least 256); 0 for an invalid shape. */
+TLS_API size_t tls_kv4_workspace_size(const tls_shape *s);
+
+/* Quantises the rows of tokens [old_lens[b], new_lens[b]) of every sequence
+ * into the cache and, where given, brings the block summary and the label slab
+ * up to date with them: a prompt (old 0) as well as the tokens of one step.
+ *   K, V        device bf16 [B][H_kv][row_stride][d]; row r is token old_lens[b] + r
+ *   old_lens, new_lens  device int32 [B], 0 <= old <= new <= max_ctx,
+ *               new - old <= row_stride; another range leaves the sequence
+ *               untouched and sets bit 4 of the device error word
+ *   row_stride  rows per (sequence, KV head) in K and V, at most max_ctx (0: no-op)
+ *   meta        the block summary of tls_build_block_meta, right for the tokens
+ *               below old_lens, or NULL; afterwards it holds the bits that
+ *               tls_build_block_meta gives for all given rows (the rows as
+ *               given, not as stored)
+ *   slab, label_idx  the label slab and its channels, or NULL; an int8 slab
+ *               returns TLS_ERR_UNSUPPORTED (rebuild it) */
+TLS_API tls_status tls_kv4_append(const tls_shape *s, const void *K, const void *V, const int32_t *old_lens,
+                                  const int32_t *new_lens, int32_t row_stride, const int32_t *label_idx, void *cache,
+                                  void *meta, void *slab, void *stream);
+
+/* The stored values of tokens [old_lens[b], new_lens[b]) as bf16 (exact), in
+ * tls_kv4_append's row layout; K_out or V_out may be NULL.  For example to
+ * rebuild the summary after an eviction (tls_build_block_meta). */
+TLS_API tls_status tls_kv4_read(const tls_shape *s, const void *cache, const int32_t *old_lens,
+                                const int32_t *new_lens, int32_t row_stride, void *K_out, void *V_out, void *stream);
+
+/* tls_sparse_attn_decode over a 4-bit cache: o_h = sum_t softmax(tau q_h.K_t) V_t
+ * and lse_h, with K_t, V_t the stored values.
+ *   q          device bf16 [B][H_q][d]
+ *   token_idx  device int32 [B][H_kv][k_t]; entries < 0 or >= max_ctx are
+ *              skipped.  NULL: every token below seq_lens[b]
+ *   seq_lens   device int32 [B]; read only without token_idx (else may be NULL)
+ *   slot_of_block, n_slots  NULL, 0, or a slot cache of blocks: cache is then
+ *              [B][H_kv][n_slots][bs] records, and token t of a group is record
+ *              t % bs of slot slot_of_block[b][g][t / bs] (-1: skipped).  With
+ *              token_idx only; n_slots * bs within int32
+ *   out, lse_out  as in tls_sparse_attn_decode (no token: out 0, lse -inf)
+ *   ws, ws_bytes  tls_kv4_workspace_size(s) bytes, 256-byte aligned; calls that
+ *              run concurrently need separate ones */
+TLS_API tls_status tls_kv4_attn_decode(const tls_shape *s, const void *q, const void *cache,
+                                       const int32_t *token_idx, const int32_t *seq_lens,
+                                       const int32_t *slot_of_block, int32_t n_slots, void *out, float *lse_out,
+                                       void *ws, size_t ws_bytes, void *stream);
+
+/* ---- eviction by accumulated attention weight ---------------------------------
+ * (no counterpart in the paper: an addition of this library.)  A decode loop
+ * adds up the attention weight of every cached token; when the cache has to
+ * shrink, the tokens with the largest sums stay. */
+
+/* weights[b][g][t] += sum over the group's heads h of exp(tau q_h.K_t - lse_h).
+ *   K          device [B][H_kv][max_ctx][d_qk] (any supported shape, MLA too)
+ *   token_idx  device int32 [B][H_kv][k_t], entries < 0 or >= max_ctx skipped (a
+ *              token listed twice is added twice); NULL: every token below seq_lens[b]
+ *   seq_lens   device int32 [B]; read only without token_idx
+ *   lse        device fp32 [B][H_q], as the step's attention returned it; a
+ *              head with -inf adds nothing
+ *   weights    device fp32 [B][H_kv][max_ctx]; start from zero
+ * The order of additions is fixed: equal inputs give equal bits. */
+TLS_API tls_status tls_accum_weights(const tls_shape *s, const void *q, const void *K, const int32_t *token_idx,
+                                     const int32_t *seq_lens, const float *lse, float *weights, void *stream);
+
+/* The same over the keys of a 4-bit cache (indexed by token). */
+TLS_API tls_status tls_kv4_accum_weights(const tls_shape *s, const void *q, const void *cache,
+                                         const int32_t *token_idx, const int32_t *seq_lens, const float *lse,
+                                         float *weights, void *stream);
+
+/* The tokens that stay, per (sequence, KV head): the first n_sink, the last
+ * n_recent, and of the others those with the largest weights (equal weights:
+ * the lower index; a NaN ranks as -inf), min(seq_len, budget) in all.
+ *   budget     1 .. max_ctx; n_sink + n_recent <= budget
+ *   weights    device fp32 [B][H_kv][max_ctx]
+ *   seq_lens   device int32 [B]
+ *   keep_idx_out  device int32 [B][H_kv][budget], ascending, -1 padded
+ *   new_lens_out  device int32 [B]: min(seq_len, budget); must not overlap seq_lens */
+TLS_API tls_status tls_evict_select(const tls_shape *s, int32_t budget, int32_t n_sink, int32_t n_recent,
+                                    const float *weights, const int32_t *seq_lens, int32_t *keep_idx_out,
+                                    int32_t *new_lens_out, void *stream);
+
+/* Moves the kept rows together, in place: row keep_idx[j] of each (sequence,
+ * KV head) becomes row j.  Rows from the number of kept ones on are left as
+ * they were.  Afterwards the summary and an int8 slab are rebuilt by
+ * tls_build_block_meta (a block now holds other tokens).
+ *   keep_idx   device int32 [B][H_kv][budget], ascending and distinct, -1
+ *              padded (tls_evict_select; ids >= max_ctx are ignored)
+ *   seq_lens   device int32 [B]: the lengths before the eviction
+ *   rows       host array of n_rows (at most 8) device arrays, each
+ *              [B][H_kv][max_ctx][row_bytes[i]] bytes: K, V, a label slab, the
+ *              4-bit cache, ...; they must not overlap.  Any alignment; 16
+ *              bytes is fastest
+ *   weights    device fp32 [B][H_kv][max_ctx] or NULL: moved too, and zero from
+ *              the last kept token to seq_lens[b] so that new tokens start at 0 */
+TLS_API tls_status tls_evict_compact(const tls_shape *s, int32_t budget, const int32_t *keep_idx,
+                                     const int32_t *seq_lens, int32_t n_rows, void *const *rows,
+                                     const int32_t *row_bytes, float *weights, void *stream);
+
 /* Stages 1+2 for callers that cannot allocate device memory (no counterpart in
  * the paper: an addition of this library).  Computes exactly what
  * tls_block_score_topk computes, needs only the inputs and block_idx_out, and
@@ -365,7 +481,8 @@ TLS_API tls_status tls_noalloc_read_scores(float *dst, size_t count, void *strea
  * are undefined, and it sets a bit in a library-owned device word; kernels
  * that meet an argument only the device can check set a bit there too:
  *   1 = an attention kernel's wait, 2 = a selection cluster's exchange wait,
- *   4 = tls_append_tokens got a length range it could not apply.
+ *   4 = tls_append_tokens, tls_kv4_append or tls_kv4_read got a length range
+ *       it could not apply.
  * Writes the word to *flags_out (0 = no failure since the last clear) and,
  * when clear != 0, zeroes it.  Reads with a synchronous cudaMemcpy, so call it
  * after the work to check has completed. */

@@ -616,6 +616,263 @@ tls_status tls_decode_step(const tls_shape *s, const void *q, const void *meta, 
   return attn_common(s, q, K, V, token_idx_out, nullptr, 0, out, lse_out, ws, ws_bytes, stream, false, ready, seq);
 }
 
+// ---- 4-bit KV cache
+// The shape checks of every call on a 4-bit cache, and the limits of its record.
+static tls_status check_kv4(const tls_shape *s) {
+  tls_status st = check_shape(s);
+  if (st != TLS_OK) return st;
+  if (s->v_is_k_prefix) return fail(TLS_ERR_UNSUPPORTED, "the 4-bit cache holds GQA K/V rows only");
+  if (s->kv_dtype != TLS_BF16) return fail(TLS_ERR_UNSUPPORTED, "the 4-bit cache takes bf16 rows and queries");
+  return TLS_OK;
+}
+
+static tls::Kv4RowsArgs kv4_rows_args(const tls_shape *s, const void *K, const void *V, const int32_t *old_lens,
+                                      const int32_t *new_lens, int32_t row_stride, void *cache) {
+  tls::Kv4RowsArgs a{};
+  a.K = K;
+  a.V = V;
+  a.old_lens = old_lens;
+  a.new_lens = new_lens;
+  a.cache = cache;
+  a.err = tls::device_error_word();
+  a.batch = s->batch;
+  a.n_kv_heads = s->n_kv_heads;
+  a.d = s->d_qk;
+  a.block_size = s->block_size;
+  a.n_blocks_max = n_blocks_max(s);
+  a.max_ctx = s->max_ctx;
+  a.n_label = s->n_label;
+  a.row_stride = row_stride;
+  return a;
+}
+
+size_t tls_kv4_cache_bytes(const tls_shape *s) {
+  if (check_kv4(s) != TLS_OK) return 0;
+  return static_cast<size_t>(s->batch) * s->n_kv_heads * s->max_ctx * (9 * s->d_qk / 8);
+}
+
+static tls::Kv4AttnArgs kv4_attn_args(const tls_shape *s) {
+  tls::Kv4AttnArgs a{};
+  a.batch = s->batch;
+  a.n_q_heads = s->n_q_heads;
+  a.n_kv_heads = s->n_kv_heads;
+  a.d = s->d_qk;
+  a.block_size = s->block_size;
+  a.n_blocks_max = n_blocks_max(s);
+  a.max_ctx = s->max_ctx;
+  a.k_t = s->k_t;
+  a.out_dtype = s->out_dtype;
+  a.scale_log2 = scale_of(s) * 1.4426950408889634f;
+  a.num_sms = device_sms();
+  return a;
+}
+
+size_t tls_kv4_workspace_size(const tls_shape *s) {
+  if (check_kv4(s) != TLS_OK) return 0;
+  return std::max<size_t>(256, up256(tls::kv4_attn_part_floats(kv4_attn_args(s)) * sizeof(float)));
+}
+
+tls_status tls_kv4_append(const tls_shape *s, const void *K, const void *V, const int32_t *old_lens,
+                          const int32_t *new_lens, int32_t row_stride, const int32_t *label_idx, void *cache,
+                          void *meta, void *slab, void *stream) {
+  tls_status st = check_kv4(s);
+  if (st != TLS_OK) return st;
+  if (s->batch == 0 || row_stride == 0) return TLS_OK;
+  if (row_stride < 0 || row_stride > s->max_ctx)
+    return fail(TLS_ERR_INVALID_ARG, "row_stride %d outside [0, max_ctx]", row_stride);
+  CHECK_PTR(K, 16);
+  CHECK_PTR(V, 16);
+  CHECK_PTR(old_lens, 4);
+  CHECK_PTR(new_lens, 4);
+  CHECK_PTR(cache, 16);
+  if (meta) CHECK_PTR(meta, 16);
+  if (slab) {
+    if (s->slab_bits == 8)  // an append can move a channel's scale and so every code of the group
+      return fail(TLS_ERR_UNSUPPORTED, "tls_kv4_append does not update an int8 label slab; rebuild it");
+    CHECK_PTR(label_idx, 4);
+    CHECK_PTR(slab, 16);
+  }
+  tls::Kv4RowsArgs a = kv4_rows_args(s, K, V, old_lens, new_lens, row_stride, cache);
+  a.label_idx = label_idx;
+  a.meta = meta;
+  a.slab = slab;
+  return cuda_status(tls::launch_kv4_append(a, static_cast<cudaStream_t>(stream)), "kv4_append launch");
+}
+
+tls_status tls_kv4_read(const tls_shape *s, const void *cache, const int32_t *old_lens, const int32_t *new_lens,
+                        int32_t row_stride, void *K_out, void *V_out, void *stream) {
+  tls_status st = check_kv4(s);
+  if (st != TLS_OK) return st;
+  if (s->batch == 0 || row_stride == 0) return TLS_OK;
+  if (row_stride < 0 || row_stride > s->max_ctx)
+    return fail(TLS_ERR_INVALID_ARG, "row_stride %d outside [0, max_ctx]", row_stride);
+  CHECK_PTR(cache, 16);
+  CHECK_PTR(old_lens, 4);
+  CHECK_PTR(new_lens, 4);
+  if (!K_out && !V_out) return fail(TLS_ERR_INVALID_ARG, "K_out and V_out are both NULL");
+  if (K_out) CHECK_PTR(K_out, 16);
+  if (V_out) CHECK_PTR(V_out, 16);
+  return cuda_status(tls::launch_kv4_read(kv4_rows_args(s, K_out, V_out, old_lens, new_lens, row_stride,
+                                                        const_cast<void *>(cache)),
+                                          static_cast<cudaStream_t>(stream)),
+                     "kv4_read launch");
+}
+
+tls_status tls_kv4_attn_decode(const tls_shape *s, const void *q, const void *cache, const int32_t *token_idx,
+                               const int32_t *seq_lens, const int32_t *slot_of_block, int32_t n_slots, void *out,
+                               float *lse_out, void *ws, size_t ws_bytes, void *stream) {
+  tls_status st = check_kv4(s);
+  if (st != TLS_OK) return st;
+  if (s->batch == 0) return TLS_OK;
+  CHECK_PTR(q, 16);
+  CHECK_PTR(cache, 16);
+  if (token_idx) CHECK_PTR(token_idx, 4);
+  else CHECK_PTR(seq_lens, 4);
+  if (slot_of_block) {
+    if (!token_idx) return fail(TLS_ERR_UNSUPPORTED, "a slot cache is attended through token_idx");
+    CHECK_PTR(slot_of_block, 4);
+    if (n_slots < 1) return fail(TLS_ERR_INVALID_ARG, "n_slots < 1");
+    if (static_cast<long long>(n_slots) * s->block_size > INT32_MAX)
+      return fail(TLS_ERR_UNSUPPORTED, "n_slots * block_size exceeds the int32 range");
+  }
+  CHECK_PTR(out, 16);
+  if (lse_out) CHECK_PTR(lse_out, 4);
+  const size_t need = tls_kv4_workspace_size(s);
+  if (!ws || ws_bytes < need || !aligned(ws, 256))
+    return fail(TLS_ERR_WORKSPACE, "workspace too small or not 256-byte aligned (need %zu bytes)", need);
+  tls::Kv4AttnArgs a = kv4_attn_args(s);
+  a.q = q;
+  a.cache = cache;
+  a.token_idx = token_idx;
+  a.seq_lens = seq_lens;
+  a.slot_of_block = slot_of_block;
+  a.n_slots = n_slots;
+  a.out = out;
+  a.lse = lse_out;
+  a.part = static_cast<float *>(ws);
+  return cuda_status(tls::launch_kv4_attention(a, static_cast<cudaStream_t>(stream)), "kv4_attention launch");
+}
+
+// ---- accumulated attention weight, eviction
+static tls_status accum_weights(const tls_shape *s, const void *q, const void *keys, int kind,
+                                const int32_t *token_idx, const int32_t *seq_lens, const float *lse, float *weights,
+                                void *stream) {
+  if (s->batch == 0) return TLS_OK;
+  CHECK_PTR(q, 16);
+  CHECK_PTR(keys, 16);
+  if (token_idx) CHECK_PTR(token_idx, 4);
+  else CHECK_PTR(seq_lens, 4);
+  CHECK_PTR(lse, 4);
+  CHECK_PTR(weights, 4);
+  tls::WeightsArgs a{};
+  a.q = q;
+  a.keys = keys;
+  a.token_idx = token_idx;
+  a.seq_lens = seq_lens;
+  a.lse = lse;
+  a.weights = weights;
+  a.batch = s->batch;
+  a.n_q_heads = s->n_q_heads;
+  a.n_kv_heads = s->n_kv_heads;
+  a.d = s->d_qk;
+  a.max_ctx = s->max_ctx;
+  a.k_t = s->k_t;
+  a.keys_kind = kind;
+  a.scale = scale_of(s);
+  a.num_sms = device_sms();
+  return cuda_status(tls::launch_accum_weights(a, static_cast<cudaStream_t>(stream)), "accum_weights launch");
+}
+
+tls_status tls_accum_weights(const tls_shape *s, const void *q, const void *K, const int32_t *token_idx,
+                             const int32_t *seq_lens, const float *lse, float *weights, void *stream) {
+  tls_status st = check_shape(s);
+  if (st != TLS_OK) return st;
+  return accum_weights(s, q, K, s->kv_dtype == TLS_BF16 ? 1 : 0, token_idx, seq_lens, lse, weights, stream);
+}
+
+tls_status tls_kv4_accum_weights(const tls_shape *s, const void *q, const void *cache, const int32_t *token_idx,
+                                 const int32_t *seq_lens, const float *lse, float *weights, void *stream) {
+  tls_status st = check_kv4(s);
+  if (st != TLS_OK) return st;
+  return accum_weights(s, q, cache, 2, token_idx, seq_lens, lse, weights, stream);
+}
+
+static tls_status check_evict(const tls_shape *s, int32_t budget) {
+  tls_status st = check_shape(s);
+  if (st != TLS_OK) return st;
+  if (budget < 1 || budget > s->max_ctx) return fail(TLS_ERR_INVALID_ARG, "budget %d outside [1, max_ctx]", budget);
+  return TLS_OK;
+}
+
+static bool overlap(const void *p, size_t np, const void *q, size_t nq) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + nq && b < a + np;
+}
+
+tls_status tls_evict_select(const tls_shape *s, int32_t budget, int32_t n_sink, int32_t n_recent,
+                            const float *weights, const int32_t *seq_lens, int32_t *keep_idx_out,
+                            int32_t *new_lens_out, void *stream) {
+  tls_status st = check_evict(s, budget);
+  if (st != TLS_OK) return st;
+  if (n_sink < 0 || n_recent < 0 || static_cast<long long>(n_sink) + n_recent > budget)
+    return fail(TLS_ERR_INVALID_ARG, "n_sink (%d) and n_recent (%d) must be >= 0 and fit the budget (%d)", n_sink,
+                n_recent, budget);
+  if (s->batch == 0) return TLS_OK;
+  CHECK_PTR(weights, 4);
+  CHECK_PTR(seq_lens, 4);
+  CHECK_PTR(keep_idx_out, 4);
+  CHECK_PTR(new_lens_out, 4);
+  const size_t lens_bytes = static_cast<size_t>(s->batch) * sizeof(int32_t);
+  if (overlap(seq_lens, lens_bytes, new_lens_out, lens_bytes))  // other CTAs still read the old lengths
+    return fail(TLS_ERR_INVALID_ARG, "new_lens_out overlaps seq_lens");
+  const tls::EvictArgs a{weights, seq_lens, keep_idx_out, new_lens_out, s->batch, s->n_kv_heads,
+                         s->max_ctx, budget, n_sink, n_recent};
+  return cuda_status(tls::launch_evict_select(a, static_cast<cudaStream_t>(stream)), "evict_select launch");
+}
+
+tls_status tls_evict_compact(const tls_shape *s, int32_t budget, const int32_t *keep_idx, const int32_t *seq_lens,
+                             int32_t n_rows, void *const *rows, const int32_t *row_bytes, float *weights,
+                             void *stream) {
+  tls_status st = check_evict(s, budget);
+  if (st != TLS_OK) return st;
+  if (n_rows < 0 || n_rows > tls::kMaxEvictRows)
+    return fail(TLS_ERR_INVALID_ARG, "n_rows %d outside [0, %d]", n_rows, tls::kMaxEvictRows);
+  if (n_rows > 0 && (!rows || !row_bytes)) return fail(TLS_ERR_INVALID_ARG, "rows or row_bytes is NULL");
+  for (int i = 0; i < n_rows; ++i) {
+    if (!rows[i]) return fail(TLS_ERR_INVALID_ARG, "rows[%d] is NULL", i);
+    if (row_bytes[i] < 1 || row_bytes[i] > 65536)
+      return fail(TLS_ERR_INVALID_ARG, "row_bytes[%d] = %d outside [1, 65536]", i, row_bytes[i]);
+  }
+  if (s->batch == 0 || (n_rows == 0 && !weights)) return TLS_OK;
+  CHECK_PTR(keep_idx, 4);
+  CHECK_PTR(seq_lens, 4);
+  if (weights) CHECK_PTR(weights, 4);
+  tls::CompactArgs a{};
+  a.n_rows = n_rows;
+  for (int i = 0; i < n_rows; ++i) {
+    a.rows[i] = rows[i];
+    a.row_bytes[i] = row_bytes[i];
+  }
+  if (weights) {
+    a.rows[a.n_rows] = weights;
+    a.row_bytes[a.n_rows++] = sizeof(float);
+  }
+  const size_t per_byte = static_cast<size_t>(s->batch) * s->n_kv_heads * s->max_ctx;
+  for (int i = 0; i < a.n_rows; ++i)  // each array is moved once, by its own CTAs
+    for (int j = 0; j < i; ++j)
+      if (overlap(a.rows[i], per_byte * a.row_bytes[i], a.rows[j], per_byte * a.row_bytes[j]))
+        return fail(TLS_ERR_INVALID_ARG, "two of the arrays to compact overlap");
+  a.weights = weights;
+  a.keep_idx = keep_idx;
+  a.seq_lens = seq_lens;
+  a.batch = s->batch;
+  a.n_kv_heads = s->n_kv_heads;
+  a.max_ctx = s->max_ctx;
+  a.budget = budget;
+  a.num_sms = device_sms();
+  return cuda_status(tls::launch_evict_compact(a, static_cast<cudaStream_t>(stream)), "evict_compact launch");
+}
+
 tls_status tls_wait_event(void *event, int32_t timeout_ms) {
   if (!event) return fail(TLS_ERR_INVALID_ARG, "event is NULL");
   if (timeout_ms < 0) timeout_ms = 0;

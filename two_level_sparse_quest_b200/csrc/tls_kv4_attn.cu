@@ -1,0 +1,581 @@
+// tls_kv4_attn.cu -- exact softmax attention of one decode step over the
+// 4-bit KV cache: over listed tokens (in the cache, or in a slot cache of
+// blocks), or over every token of each sequence.
+//
+// For query head h of a group: a_t = tau q_h . K_t, o_h = sum_t softmax(a)_t V_t,
+// lse_h = log sum_t exp(a_t), with K_t and V_t the values the record stands for.
+//
+// Bound: a token is 9 d / 8 bytes (144 at d 128), against 4 G d flop, so HBM
+// is the floor; at that rate an SM has 6.4 cycles for a token, and it is the
+// instructions that widen the codes (two for each pair of channels: e2m1 ->
+// fp16, times the scale) that come near it, not the tensor pipe.
+//
+// Layout: the tokens are the MMA rows.  S^T[16 tokens x 8 heads] = K q^T takes
+// one m16n8k16 per 16 channels, O^T[16 channels x 8 heads] += V^T P^T one per
+// 16 channels and 16 tokens: up to 8 heads cost one MMA column block, half of
+// what heads as rows would.  The order of the contraction is free, so lane c
+// of a quad takes 32 neighbouring channels of K (one 16-byte read of codes
+// and two scales) and lane group g takes 16 neighbouring channels of V (8
+// bytes and one scale) and no operand passes through another lane, except P:
+// its two fp16 parts turn from S^T's accumulator layout into the B operand
+// with movmatrix.  V's pairs (two tokens of one channel) are formed on the
+// codes, a nibble of each token in a byte, before they are widened.
+//
+// Numerics: K and V are exact in fp16; q is (tls_kv4.cuh, q_norm); sums are
+// fp32.  P is 2^(s - m + 14), below 2^15, as fp16 high and low parts (22
+// bits; what falls below 2^-38 of the largest weight is dropped): with one
+// part the fp32 output would be off by 1e-4.  m is a running reference that
+// moves only when a score exceeds it by more than one (log2).
+//
+// Work split: a unit is one group (or 16 of its heads).  A thread-block
+// cluster of up to 8 CTAs takes a unit (or one of its n_split parts), every
+// warp 32-token tiles in turn through its own cp.async ring; the warps' and
+// then the CTAs' partial (m, l, O) are joined in shared memory, the CTAs' over
+// distributed shared memory, so that one launch does the whole step.  With
+// too few units to fill the GPU (n_split > 1) the clusters leave partials in
+// the workspace and a second launch joins them.
+#include <algorithm>
+
+#include "tls_internal.h"
+#include "tls_kv4.cuh"
+#include "tls_mma.cuh"
+
+namespace tls {
+namespace {
+
+constexpr int kTile = 32;   // tokens per ring stage
+constexpr int kWarps = 8;   // per CTA
+constexpr int kRing = 3;
+constexpr int kMaxCluster = 8;
+constexpr float kPShift = 14.f;  // P is scaled by 2^14
+
+template <int D, int NT>
+struct Kv4Smem {
+  using R = Kv4Rec<D>;
+  static constexpr int kStage = kTile * R::kBytes;
+  static constexpr int kWarpBytes = kRing * kStage;
+  static constexpr int kSmem = kWarps * kWarpBytes;
+  // A warp's partial O [8 NT heads][D channels] overlays its ring.  Two words
+  // of padding per lane group's channels and a head stride of 4 mod 16 keep
+  // the 8-byte stores of a half warp in distinct banks.
+  static constexpr int kCpl = D / 8;  // channels per lane group
+  static constexpr int kHead = 8 * (kCpl + 2) + 4;
+  static_assert(kHead % 16 == 4, "bank spread of the partial's heads");
+  static_assert(8 * NT * kHead * 4 <= kWarpBytes, "the partial fits the ring");
+  static __device__ __forceinline__ int at(int head, int ch) { return head * kHead + ch + 2 * (ch / kCpl); }
+};
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async_zfill(uint32_t dst, const void *src, bool ok) {
+  const int n = ok ? BYTES : 0;
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+
+// The token (0..15 of a half) in MMA row `row` (0..7; rows 8..15 are 8 more).
+// Halves take even and odd tokens of a stage; with this order neither the
+// 16-byte reads of K (row pairs two tokens apart) nor the 8-byte reads of V
+// (rows 2c) collide in shared memory at d 128.
+__device__ __forceinline__ int row_token(int row) { return (0x57463120u >> (4 * row)) & 15; }
+
+template <int D, int NT, bool LIST, bool PAGED>
+__global__ void __launch_bounds__(kWarps * 32, 2) kv4_attn_kernel(Kv4AttnArgs a) {
+  using R = Kv4Rec<D>;
+  using L = Kv4Smem<D, NT>;
+  constexpr int KS = D / 16;   // MMA steps of S
+  constexpr int OT = D / 16;   // 16-channel tiles of O
+  constexpr int CW = D / 32;   // 32-bit words of K codes per lane and token
+  constexpr int VW = D / 64;   // 32-bit words of V codes per lane and token
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ float s_ml[kWarps][8 * NT][2];
+  __shared__ float s_cta[8 * NT][2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, c = lane & 3;
+  unsigned char *ring = smem + warp * L::kWarpBytes;
+  const uint32_t ring_s = smem_addr(ring);
+
+  const int CS = a.cluster;
+  const int rank = static_cast<int>(blockIdx.x) % CS;
+  const int part = (static_cast<int>(blockIdx.x) / CS) % a.n_split;
+  const int unit = static_cast<int>(blockIdx.x) / (CS * a.n_split);
+  const int group = unit / a.n_head_chunks, hc = unit % a.n_head_chunks;
+  const int b = group / a.n_kv_heads, gk = group % a.n_kv_heads;
+  const int G = a.n_q_heads / a.n_kv_heads;
+  const int HG = a.head_chunk;
+  const int head0 = gk * G + hc * HG;
+
+  grid_dependency_wait();
+
+  const int n = LIST ? a.k_t : min(max(a.seq_lens[b], 0), a.max_ctx);
+  const int n_tiles = (n + kTile - 1) / kTile;
+  const int per_part = (n_tiles + a.n_split - 1) / a.n_split;
+  const int t_end = min(n_tiles, (part + 1) * per_part);
+  const int stride = CS * kWarps;
+  int t_issue = part * per_part + rank * kWarps + warp;
+  const int my_tiles = t_issue < t_end ? (t_end - t_issue + stride - 1) / stride : 0;
+
+  const unsigned char *base = static_cast<const unsigned char *>(a.cache);
+  if constexpr (PAGED) base += static_cast<size_t>(group) * a.n_slots * a.block_size * R::kBytes;
+  else base += static_cast<size_t>(group) * a.max_ctx * R::kBytes;
+  const int32_t *ids = LIST ? a.token_idx + static_cast<size_t>(group) * a.k_t : nullptr;
+  const int32_t *slots = PAGED ? a.slot_of_block + static_cast<size_t>(group) * a.n_blocks_max : nullptr;
+
+  // Cache row of this lane's token of tile t, or -1.
+  auto row_of = [&](int t) -> int {
+    const int j = t * kTile + lane;
+    if (t >= t_end || j >= n) return -1;
+    if constexpr (!LIST) return j;
+    const int tok = ids[j];
+    if (tok < 0 || tok >= a.max_ctx) return -1;
+    if constexpr (!PAGED) return tok;
+    const int blk = tok / a.block_size;
+    const int slot = slots[blk];
+    return (slot >= 0 && slot < a.n_slots) ? slot * a.block_size + (tok - blk * a.block_size) : -1;
+  };
+
+  // Ring: copies of one stage are 288 chunks of D / 8 bytes, nine per lane,
+  // neighbouring lanes on neighbouring bytes.
+  uint32_t valid[kRing];  // valid tokens of the stages in flight, oldest first
+#pragma unroll
+  for (int s = 0; s < kRing; ++s) valid[s] = 0;
+  int row_next = row_of(t_issue), stage_issue = 0;
+  auto issue = [&]() -> uint32_t {
+    const int row = row_next;
+    const uint32_t mask = __ballot_sync(0xffffffffu, row >= 0);
+    if (mask != 0u) {
+      const uint32_t dst = ring_s + stage_issue * L::kStage + lane * R::kChunk;
+#pragma unroll
+      for (int i = 0; i < 9; ++i) {
+        const int idx = i * 32 + lane;
+        const int tk = (idx * 57) >> 9;  // idx / 9 for idx < 288
+        const int rw = __shfl_sync(0xffffffffu, row, tk);
+        const long long off = static_cast<long long>(rw - tk) * R::kBytes + idx * R::kChunk;
+        cp_async_zfill<R::kChunk>(dst + i * 32 * R::kChunk, base + (rw >= 0 ? off : 0), rw >= 0);
+      }
+    }
+    t_issue += stride;
+    row_next = row_of(t_issue);
+    if (++stage_issue == kRing) stage_issue = 0;
+    return mask;
+  };
+
+#pragma unroll
+  for (int s = 0; s < kRing - 1; ++s) {
+    valid[s + 1] = issue();
+    cp_async_commit();
+  }
+
+  // Queries: B fragments of S^T = K q^T.  Lane (g, c) holds head 8 nt + g's
+  // channels c D/4 .. + D/4 - 1, four per MMA step.
+  uint32_t qb[NT][KS][2];
+  float sl[NT][2];  // score scale of this lane's columns (heads 8 nt + 2c, + 1)
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int h = nt * 8 + g;
+    uint32_t w[D / 8];
+    uint32_t ex = 0;
+    const uint4 *qp = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) +
+                                                      (static_cast<size_t>(b) * a.n_q_heads + head0 + h) * D + c * (D / 4));
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint4 v = h < HG ? qp[i] : make_uint4(0u, 0u, 0u, 0u);
+      w[4 * i] = v.x;
+      w[4 * i + 1] = v.y;
+      w[4 * i + 2] = v.z;
+      w[4 * i + 3] = v.w;
+    }
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) ex = max(ex, bf16_exps(w[i]));
+    ex = max(ex, __shfl_xor_sync(0xffffffffu, ex, 1));
+    ex = max(ex, __shfl_xor_sync(0xffffffffu, ex, 2));
+    float undo;
+    const float mult = q_norm(ex, &undo);
+#pragma unroll
+    for (int j = 0; j < KS; ++j) {
+      qb[nt][j][0] = q_to_f16(w[2 * j], mult);
+      qb[nt][j][1] = q_to_f16(w[2 * j + 1], mult);
+    }
+    sl[nt][0] = a.scale_log2 * __shfl_sync(0xffffffffu, undo, 8 * c);
+    sl[nt][1] = a.scale_log2 * __shfl_sync(0xffffffffu, undo, 8 * c + 4);
+  }
+
+  float o[NT][OT][4];
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int j = 0; j < OT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[nt][j][e] = 0.f;
+    m[nt][0] = m[nt][1] = -INFINITY;
+    l[nt][0] = l[nt][1] = 0.f;
+  }
+
+  const int ktok = 2 * row_token(g);  // this lane's K rows: tokens ktok + half, ktok + 16 + half
+  const int vtok0 = 2 * row_token(2 * c), vtok1 = 2 * row_token(2 * c + 1);
+
+  int st = 0;
+  for (int it = 0; it < my_tiles; ++it) {
+#pragma unroll
+    for (int s = 0; s + 1 < kRing; ++s) valid[s] = valid[s + 1];
+    valid[kRing - 1] = issue();
+    cp_async_commit();
+    cp_async_wait<kRing - 1>();
+    __syncwarp();
+    const uint32_t vm = valid[0];
+    if (vm != 0u) {
+      const unsigned char *S = ring + st * L::kStage;
+      float s[2][NT][4];  // [half]: rows g, g + 8 of heads 2c, 2c + 1
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[hf][nt][e] = 0.f;
+        const unsigned char *k0 = S + (ktok + hf) * R::kBytes, *k1 = k0 + 16 * R::kBytes;
+        uint32_t w0[CW], w1[CW], sc0, sc1;
+        if constexpr (D == 128) {
+          *reinterpret_cast<uint4 *>(w0) = *reinterpret_cast<const uint4 *>(k0 + 16 * c);
+          *reinterpret_cast<uint4 *>(w1) = *reinterpret_cast<const uint4 *>(k1 + 16 * c);
+          sc0 = *reinterpret_cast<const uint16_t *>(k0 + R::kKS + 2 * c);
+          sc1 = *reinterpret_cast<const uint16_t *>(k1 + R::kKS + 2 * c);
+        } else {
+          *reinterpret_cast<uint2 *>(w0) = *reinterpret_cast<const uint2 *>(k0 + 8 * c);
+          *reinterpret_cast<uint2 *>(w1) = *reinterpret_cast<const uint2 *>(k1 + 8 * c);
+          sc0 = k0[R::kKS + c];
+          sc1 = k1[R::kKS + c];
+        }
+#pragma unroll
+        for (int w = 0; w < CW; ++w) {
+          // words 0, 1 of a row lie in the lane's first group of 16 channels, 2, 3 in its second
+          const uint32_t f0 = (w < 2 ? sc0 & 0xffu : sc0 >> 8) * 0x00800080u;
+          const uint32_t f1 = (w < 2 ? sc1 & 0xffu : sc1 >> 8) * 0x00800080u;
+          uint32_t x[4], y[4];
+          e2m1_unpack(w0[w], x[0], x[1], x[2], x[3]);
+          e2m1_unpack(w1[w], y[0], y[1], y[2], y[3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[e] = hmul2(x[e], f0);
+            y[e] = hmul2(y[e], f1);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_f16(s[hf][nt], x[0], y[0], x[1], y[1], qb[nt][2 * w][0], qb[nt][2 * w][1]);
+            mma_f16(s[hf][nt], x[2], y[2], x[3], y[3], qb[nt][2 * w + 1][0], qb[nt][2 * w + 1][1]);
+          }
+        }
+      }
+      // ---- online softmax in the log2 domain
+      bool over = false;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const bool ok0 = (vm >> (ktok + hf)) & 1u, ok1 = (vm >> (ktok + 16 + hf)) & 1u;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[hf][nt][e] = (e < 2 ? ok0 : ok1) ? s[hf][nt][e] * sl[nt][e & 1] : -INFINITY;
+            over |= s[hf][nt][e] > m[nt][e & 1] + 1.f;
+          }
+      }
+      if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            if (mx > m[nt][e]) {
+              const float alpha = ex2(m[nt][e] - mx);  // 0 for the first tokens
+              m[nt][e] = mx;
+              l[nt][e] *= alpha;
+#pragma unroll
+              for (int j = 0; j < OT; ++j) {
+                o[nt][j][e] *= alpha;
+                o[nt][j][e + 2] *= alpha;
+              }
+            }
+          }
+      }
+      // ---- O^T += V^T P^T
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float mm = m[nt][e & 1];
+            p[e] = ex2(s[hf][nt][e] - (mm == -INFINITY ? 0.f : mm) + kPShift);
+            l[nt][e & 1] += p[e];
+          }
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const __half2 hi = __floats2half2_rn(p[2 * r], p[2 * r + 1]);
+            const float2 hf2 = __half22float2(hi);
+            const __half2 lo = __floats2half2_rn(p[2 * r] - hf2.x, p[2 * r + 1] - hf2.y);
+            ph[nt][r] = movmatrix(*reinterpret_cast<const uint32_t *>(&hi));
+            pl[nt][r] = movmatrix(*reinterpret_cast<const uint32_t *>(&lo));
+          }
+        }
+        const unsigned char *v0 = S + (vtok0 + hf) * R::kBytes, *v1 = S + (vtok1 + hf) * R::kBytes;
+        constexpr int V8 = 16 * R::kBytes;  // rows 8 more: 16 tokens on
+        uint32_t w[4][VW], sc[2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const unsigned char *v = (i & 1 ? v1 : v0) + (i >> 1) * V8;
+          if constexpr (D == 128) *reinterpret_cast<uint2 *>(w[i]) = *reinterpret_cast<const uint2 *>(v + R::kVC + 8 * g);
+          else w[i][0] = *reinterpret_cast<const uint32_t *>(v + R::kVC + 4 * g);
+        }
+        // a lane group's channels share one scale (d 64: half of one)
+        constexpr int SD = D == 128 ? 1 : 2;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t a0 = v0[r * V8 + R::kVS + g / SD], a1 = v1[r * V8 + R::kVS + g / SD];
+          sc[r] = (a0 << 7) | (a1 << 23);
+        }
+#pragma unroll
+        for (int q = 0; q < VW; ++q) {
+          // bytes of one channel from two tokens: even channels, odd channels
+          uint32_t ev[2][4], od[2][4];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const uint32_t x = w[2 * r][q], y = w[2 * r + 1][q];
+            e2m1_unpack((x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u), ev[r][0], ev[r][1], ev[r][2], ev[r][3]);
+            e2m1_unpack(((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u), od[r][0], od[r][1], od[r][2], od[r][3]);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t a0 = hmul2(ev[0][j], sc[0]), a1 = hmul2(od[0][j], sc[0]);
+            const uint32_t a2 = hmul2(ev[1][j], sc[1]), a3 = hmul2(od[1][j], sc[1]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_f16(o[nt][4 * q + j], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+              mma_f16(o[nt][4 * q + j], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();
+    if (++st == kRing) st = 0;
+  }
+  cp_async_wait<0>();
+  __syncwarp();
+
+  // ---- the warp's partial into its own ring
+  float *po = reinterpret_cast<float *>(ring);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float t = l[nt][e];
+      t += __shfl_xor_sync(0xffffffffu, t, 4);
+      t += __shfl_xor_sync(0xffffffffu, t, 8);
+      t += __shfl_xor_sync(0xffffffffu, t, 16);
+      const int h = nt * 8 + 2 * c + e;
+      if (g == 0) {
+        s_ml[warp][h][0] = m[nt][e];
+        s_ml[warp][h][1] = t;
+      }
+#pragma unroll
+      for (int j = 0; j < OT; ++j)
+        *reinterpret_cast<float2 *>(po + L::at(h, g * L::kCpl + 2 * j)) = make_float2(o[nt][j][e], o[nt][j][e + 2]);
+    }
+  }
+  __syncthreads();
+
+  // ---- joined over the CTA's warps (a warp without a token has m = -inf, l = 0)
+  float *cta_o = reinterpret_cast<float *>(smem);
+  const int n_out = HG * D;
+  for (int i = threadIdx.x; i < n_out; i += kWarps * 32) {
+    const int h = i / D, ch = i % D;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w][h][0]);
+    const float Mu = M == -INFINITY ? 0.f : M;
+    float acc = 0.f, ls = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = ex2(s_ml[w][h][0] - Mu);
+      ls = fmaf(f, s_ml[w][h][1], ls);
+      acc = fmaf(f, reinterpret_cast<const float *>(smem + w * L::kWarpBytes)[L::at(h, ch)], acc);
+    }
+    cta_o[L::at(h, ch)] = acc;  // warp 0's element (h, ch): read by this thread only
+    if (ch == 0) {
+      s_cta[h][0] = M;
+      s_cta[h][1] = ls;
+    }
+  }
+  if (CS > 1) {
+    cluster_arrive_release();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+
+  // ---- joined over the cluster: each CTA writes a share of the outputs
+  const size_t n_units = static_cast<size_t>(a.batch) * a.n_kv_heads * a.n_head_chunks;
+  for (int i = rank * (kWarps * 32) + threadIdx.x; i < n_out; i += CS * kWarps * 32) {
+    const int h = i / D, ch = i % D;
+    float M, ls, acc;
+    if (CS == 1) {
+      M = s_cta[h][0];
+      ls = s_cta[h][1];
+      acc = cta_o[L::at(h, ch)];
+    } else {
+      const uint32_t am = smem_addr(&s_cta[h][0]), ao = smem_addr(cta_o + L::at(h, ch));
+      float mr[kMaxCluster], lr[kMaxCluster], orr[kMaxCluster];
+      M = -INFINITY;
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        mr[r] = r < CS ? ld_cluster(cluster_map(am, r)) : -INFINITY;
+        lr[r] = r < CS ? ld_cluster(cluster_map(am, r) + 4) : 0.f;
+        orr[r] = r < CS ? ld_cluster(cluster_map(ao, r)) : 0.f;
+        M = fmaxf(M, mr[r]);
+      }
+      const float Mu = M == -INFINITY ? 0.f : M;
+      ls = acc = 0.f;
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        const float f = ex2(mr[r] - Mu);
+        ls = fmaf(f, lr[r], ls);
+        acc = fmaf(f, orr[r], acc);
+      }
+    }
+    if (a.n_split > 1) {
+      float *ml = a.part + (static_cast<size_t>(unit) * a.n_split + part) * HG * 2;
+      float *pp = a.part + n_units * a.n_split * HG * 2 + (static_cast<size_t>(unit) * a.n_split + part) * n_out;
+      pp[i] = acc;
+      if (ch == 0) {
+        ml[2 * h] = M;
+        ml[2 * h + 1] = ls;
+      }
+    } else {
+      const float res = ls == 0.f ? 0.f : acc / ls;
+      const size_t head = static_cast<size_t>(b) * a.n_q_heads + head0 + h;
+      if (a.out_dtype == 1) static_cast<__nv_bfloat16 *>(a.out)[head * D + ch] = __float2bfloat16_rn(res);
+      else static_cast<float *>(a.out)[head * D + ch] = res;
+      if (a.lse && ch == 0) a.lse[head] = ls == 0.f ? -INFINITY : (M + (log2f(ls) - kPShift)) * 0.69314718055994531f;
+    }
+  }
+  if (CS > 1) {  // no CTA leaves while another reads its shared memory
+    cluster_arrive_release();
+    cluster_wait();
+  }
+}
+
+// Joins the n_split partials of each unit: one thread per (head, channel).
+template <int D>
+__global__ void __launch_bounds__(128) kv4_merge_kernel(Kv4AttnArgs a) {
+  grid_dependency_wait();
+  const int unit = blockIdx.y;
+  const int i = blockIdx.x * 128 + threadIdx.x;
+  const int HG = a.head_chunk;
+  if (i >= HG * D) return;
+  const int h = i / D, ch = i % D;
+  const size_t n_units = static_cast<size_t>(a.batch) * a.n_kv_heads * a.n_head_chunks;
+  const float *ml = a.part + static_cast<size_t>(unit) * a.n_split * HG * 2 + 2 * h;
+  const float *po = a.part + n_units * a.n_split * HG * 2 + static_cast<size_t>(unit) * a.n_split * HG * D + i;
+  float M = -INFINITY;
+  for (int p = 0; p < a.n_split; ++p) M = fmaxf(M, ml[static_cast<size_t>(p) * HG * 2]);
+  const float Mu = M == -INFINITY ? 0.f : M;
+  float ls = 0.f, acc = 0.f;
+#pragma unroll 8
+  for (int p = 0; p < a.n_split; ++p) {
+    const float f = ex2(ml[static_cast<size_t>(p) * HG * 2] - Mu);
+    ls = fmaf(f, ml[static_cast<size_t>(p) * HG * 2 + 1], ls);
+    acc = fmaf(f, po[static_cast<size_t>(p) * HG * D], acc);
+  }
+  const int group = unit / a.n_head_chunks, hc = unit % a.n_head_chunks;
+  const int b = group / a.n_kv_heads, gk = group % a.n_kv_heads;
+  const size_t head = static_cast<size_t>(b) * a.n_q_heads + gk * (a.n_q_heads / a.n_kv_heads) + hc * HG + h;
+  const float res = ls == 0.f ? 0.f : acc / ls;
+  if (a.out_dtype == 1) static_cast<__nv_bfloat16 *>(a.out)[head * D + ch] = __float2bfloat16_rn(res);
+  else static_cast<float *>(a.out)[head * D + ch] = res;
+  if (a.lse && ch == 0) a.lse[head] = ls == 0.f ? -INFINITY : (M + (log2f(ls) - kPShift)) * 0.69314718055994531f;
+}
+
+// How a call is cut: heads per unit, CTAs per cluster, clusters per unit.
+void kv4_plan(Kv4AttnArgs &a, int n_max) {
+  const int G = a.n_q_heads / a.n_kv_heads;
+  a.head_chunk = std::min(G, 16);
+  a.n_head_chunks = G / a.head_chunk;
+  const long long units = static_cast<long long>(a.batch) * a.n_kv_heads * a.n_head_chunks;
+  const int sms = a.num_sms > 0 ? a.num_sms : 148;
+  const long long slots = 2LL * sms;                               // CTAs resident at once
+  const long long tiles = (n_max + kTile - 1) / kTile;             // of one unit
+  const long long most = (tiles + kWarps - 1) / kWarps;            // CTAs that still have a tile for every warp
+  int cs = 1;
+  while (cs < kMaxCluster && cs * 2 <= most && units * cs < slots) cs *= 2;
+  a.cluster = cs;
+  a.n_split = 1;
+  if (cs == kMaxCluster && units * cs * 2 <= slots)
+    a.n_split = static_cast<int>(std::min<long long>(slots / (units * cs), std::max<long long>(1, most / cs)));
+}
+
+template <int D, int NT, bool LIST, bool PAGED>
+cudaError_t run(const Kv4AttnArgs &a, cudaStream_t st) {
+  using L = Kv4Smem<D, NT>;
+  auto kern = kv4_attn_kernel<D, NT, LIST, PAGED>;
+  static bool configured[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !configured[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) configured[dev] = true;
+  }
+  const long long ctas = static_cast<long long>(a.batch) * a.n_kv_heads * a.n_head_chunks * a.n_split * a.cluster;
+  return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(ctas)), dim3(kWarps * 32), L::kSmem, st, a.cluster, a);
+}
+
+template <int D, int NT>
+cudaError_t dispatch(const Kv4AttnArgs &a, cudaStream_t st) {
+  if (!a.token_idx) return run<D, NT, false, false>(a, st);
+  return a.slot_of_block ? run<D, NT, true, true>(a, st) : run<D, NT, true, false>(a, st);
+}
+
+}  // namespace
+
+size_t kv4_attn_part_floats(const Kv4AttnArgs &in) {
+  size_t most = 0;
+  for (int n : {in.k_t, in.max_ctx}) {
+    Kv4AttnArgs a = in;
+    kv4_plan(a, n);
+    if (a.n_split == 1) continue;
+    const size_t units = static_cast<size_t>(a.batch) * a.n_kv_heads * a.n_head_chunks;
+    most = std::max(most, units * a.n_split * a.head_chunk * (2 + a.d));
+  }
+  return most;
+}
+
+cudaError_t launch_kv4_attention(Kv4AttnArgs a, cudaStream_t st) {
+  kv4_plan(a, a.token_idx ? a.k_t : a.max_ctx);
+  cudaError_t e;
+  if (a.d == 128) e = a.head_chunk > 8 ? dispatch<128, 2>(a, st) : dispatch<128, 1>(a, st);
+  else e = a.head_chunk > 8 ? dispatch<64, 2>(a, st) : dispatch<64, 1>(a, st);
+  if (e != cudaSuccess || a.n_split == 1) return e;
+  const dim3 grid((a.head_chunk * a.d + 127) / 128, a.batch * a.n_kv_heads * a.n_head_chunks);
+  if (a.d == 128) return launch_pdl(kv4_merge_kernel<128>, grid, dim3(128), 0, st, a);
+  return launch_pdl(kv4_merge_kernel<64>, grid, dim3(128), 0, st, a);
+}
+
+}  // namespace tls

@@ -31,7 +31,9 @@ STATUS_NAMES = {0: "TLS_OK", 1: "TLS_ERR_INVALID_ARG", 2: "TLS_ERR_UNSUPPORTED",
 EXPORTED = ("tls_version", "tls_last_error", "tls_workspace_size", "tls_build_block_meta", "tls_block_score_topk",
             "tls_token_score_topk", "tls_sparse_attn_decode", "tls_sparse_attn_decode_paged", "tls_offload_reset",
             "tls_prefetch_diff", "tls_wait_event", "tls_block_score_topk_noalloc", "tls_device_error", "tls_select_step",
-            "tls_append_tokens", "tls_slab_bytes", "tls_noalloc_read_scores", "tls_decode_step", "tls_select_step_ws")
+            "tls_append_tokens", "tls_slab_bytes", "tls_noalloc_read_scores", "tls_decode_step", "tls_select_step_ws",
+            "tls_kv4_cache_bytes", "tls_kv4_workspace_size", "tls_kv4_append", "tls_kv4_read", "tls_kv4_attn_decode",
+            "tls_accum_weights", "tls_kv4_accum_weights", "tls_evict_select", "tls_evict_compact")
 
 
 class TlsShape(ctypes.Structure):
@@ -75,6 +77,15 @@ _sigs = {
     "tls_noalloc_read_scores": ([_P, _sz, _P], ctypes.c_int),
     "tls_decode_step": ([_S, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _sz, _P], ctypes.c_int),
     "tls_select_step_ws": ([_S, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _sz, _P], ctypes.c_int),
+    "tls_kv4_cache_bytes": ([_S], _sz),
+    "tls_kv4_workspace_size": ([_S], _sz),
+    "tls_kv4_append": ([_S, _P, _P, _P, _P, _i32, _P, _P, _P, _P, _P], ctypes.c_int),
+    "tls_kv4_read": ([_S, _P, _P, _P, _i32, _P, _P, _P], ctypes.c_int),
+    "tls_kv4_attn_decode": ([_S, _P, _P, _P, _P, _P, _i32, _P, _P, _P, _sz, _P], ctypes.c_int),
+    "tls_accum_weights": ([_S, _P, _P, _P, _P, _P, _P, _P], ctypes.c_int),
+    "tls_kv4_accum_weights": ([_S, _P, _P, _P, _P, _P, _P, _P], ctypes.c_int),
+    "tls_evict_select": ([_S, _i32, _i32, _i32, _P, _P, _P, _P, _P], ctypes.c_int),
+    "tls_evict_compact": ([_S, _i32, _P, _P, _i32, ctypes.POINTER(_P), ctypes.POINTER(_i32), _P, _P], ctypes.c_int),
 }
 for _name, (_args, _ret) in _sigs.items():
     _f = getattr(_lib, _name)
@@ -256,6 +267,84 @@ def tls_prefetch_diff(shape, n_slots, host_kv, cache, slot_of_block, block_of_sl
                                   _dptr(jobs_ws), _stream(stream)), "tls_prefetch_diff")
 
 
+def tls_kv4_cache_bytes(shape: TlsShape) -> int:
+    n = _lib.tls_kv4_cache_bytes(ctypes.byref(shape))
+    if n == 0 and shape.batch != 0:
+        raise TlsError(TLS_ERR_UNSUPPORTED, f"tls_kv4_cache_bytes: {tls_last_error()}")
+    return n
+
+
+def tls_kv4_workspace_size(shape: TlsShape) -> int:
+    n = _lib.tls_kv4_workspace_size(ctypes.byref(shape))
+    if n == 0:
+        raise TlsError(TLS_ERR_UNSUPPORTED, f"tls_kv4_workspace_size: {tls_last_error()}")
+    return n
+
+
+def tls_kv4_append(shape, K, V, old_lens, new_lens, row_stride, cache, label_idx=None, meta=None, slab=None,
+                   stream=None):
+    """Quantises the rows of tokens [old_lens, new_lens) into the 4-bit cache; with meta / slab given, brings the
+    block summary and the label slab up to date with them."""
+    _check(_lib.tls_kv4_append(ctypes.byref(shape), _dptr(K), _dptr(V), _dptr(old_lens), _dptr(new_lens),
+                               int(row_stride), _dptr(label_idx), _dptr(cache), _dptr(meta), _dptr(slab),
+                               _stream(stream)), "tls_kv4_append")
+
+
+def tls_kv4_read(shape, cache, old_lens, new_lens, row_stride, K_out=None, V_out=None, stream=None):
+    """The stored values of tokens [old_lens, new_lens) as bf16 rows."""
+    _check(_lib.tls_kv4_read(ctypes.byref(shape), _dptr(cache), _dptr(old_lens), _dptr(new_lens), int(row_stride),
+                             _dptr(K_out), _dptr(V_out), _stream(stream)), "tls_kv4_read")
+
+
+def tls_kv4_attn_decode(shape, q, cache, out, lse_out=None, token_idx=None, seq_lens=None, slot_of_block=None,
+                        n_slots=0, ws=None, stream=None):
+    """Attention over a 4-bit cache: the tokens of token_idx, or without it every token below seq_lens."""
+    wp, wb = _ws(ws)
+    _check(_lib.tls_kv4_attn_decode(ctypes.byref(shape), _dptr(q), _dptr(cache), _dptr(token_idx), _dptr(seq_lens),
+                                    _dptr(slot_of_block), int(n_slots), _dptr(out), _dptr(lse_out), wp, wb,
+                                    _stream(stream)), "tls_kv4_attn_decode")
+
+
+def tls_accum_weights(shape, q, K, lse, weights, token_idx=None, seq_lens=None, stream=None):
+    """Adds the step's attention weights, summed over each group's heads, to one fp32 number per token."""
+    _check(_lib.tls_accum_weights(ctypes.byref(shape), _dptr(q), _dptr(K), _dptr(token_idx), _dptr(seq_lens),
+                                  _dptr(lse), _dptr(weights), _stream(stream)), "tls_accum_weights")
+
+
+def tls_kv4_accum_weights(shape, q, cache, lse, weights, token_idx=None, seq_lens=None, stream=None):
+    """tls_accum_weights over the keys of a 4-bit cache."""
+    _check(_lib.tls_kv4_accum_weights(ctypes.byref(shape), _dptr(q), _dptr(cache), _dptr(token_idx),
+                                      _dptr(seq_lens), _dptr(lse), _dptr(weights), _stream(stream)),
+           "tls_kv4_accum_weights")
+
+
+def tls_evict_select(shape, budget, n_sink, n_recent, weights, seq_lens, keep_idx_out, new_lens_out, stream=None):
+    """The tokens that stay: the first n_sink, the last n_recent, the rest by weight, `budget` in all."""
+    _check(_lib.tls_evict_select(ctypes.byref(shape), int(budget), int(n_sink), int(n_recent), _dptr(weights),
+                                 _dptr(seq_lens), _dptr(keep_idx_out), _dptr(new_lens_out), _stream(stream)),
+           "tls_evict_select")
+
+
+def tls_evict_compact(shape, budget, keep_idx, seq_lens, rows, weights=None, stream=None):
+    """Moves the kept rows together in place.  rows: CUDA tensors of shape [B, H_kv, max_ctx, ...] (any element
+    type), or (pointer, bytes of a row) pairs."""
+    ptrs, sizes = [], []
+    for x in rows:
+        if isinstance(x, torch.Tensor):
+            want = (shape.batch, shape.n_kv_heads, shape.max_ctx)
+            if tuple(x.shape[:3]) != want:
+                raise ValueError(f"rows tensors start with [B, H_kv, max_ctx] = {list(want)}, got {list(x.shape)}")
+            ptrs.append(_dptr(x))
+            sizes.append(math.prod(x.shape[3:]) * x.element_size())
+        else:
+            ptrs.append(x[0])
+            sizes.append(int(x[1]))
+    n = len(ptrs)
+    _check(_lib.tls_evict_compact(ctypes.byref(shape), int(budget), _dptr(keep_idx), _dptr(seq_lens), n,
+                                  (_P * max(n, 1))(*ptrs), (_i32 * max(n, 1))(*sizes), _dptr(weights),
+                                  _stream(stream)), "tls_evict_compact")
+
+
 def tls_block_score_topk_noalloc(shape, q, meta, seq_lens, block_idx_out, stream=None):
     """Block selection without a workspace, for callers that cannot allocate
     device memory: the scores live in a fixed array inside the library (see
@@ -281,7 +370,8 @@ def tls_wait_event(event, timeout_ms: int) -> int:
 
 def tls_device_error(clear: bool = False) -> int:
     """Failure flags of the current device (1: an attention wait gave up,
-    2: a selection exchange wait gave up); 0 means none since the last clear."""
+    2: a selection exchange wait gave up, 4: an append got a length range it
+    could not apply); 0 means none since the last clear."""
     v = _i32(0)
     _check(_lib.tls_device_error(ctypes.byref(v), int(bool(clear))), "tls_device_error")
     return v.value
