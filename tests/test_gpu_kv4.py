@@ -199,8 +199,10 @@ def check_attention(T, B, H, G, d, ctx, tokens, mode, out_dtype=0, bs=32, seed=5
                 t = [x for x in t if 0 <= resident[b, h, x // bs] < kw["n_slots"]]
             hs = slice(h * G, (h + 1) * G)
             wo, wl, tol, ltol = R.attention(f64(q[b, hs]), K, V, t, tau)
-            if out_dtype:
-                tol = tol + 2.0 ** -8 * (np.abs(wo) + tol)  # half a step of bf16
+            if out_dtype:  # half a step of fp16 on every weight, half a step of bf16 on the result
+                p = np.exp(f64(q[b, hs]) @ K[t].T * tau - wl[:, None]) if len(t) else np.zeros((G, 0))
+                tol = tol + 2.0 ** -11 * (p @ np.abs(V[t]))
+                tol = tol + 2.0 ** -8 * (np.abs(wo) + tol)
             over = float((np.abs(o[b, hs] - wo) / tol).max())
             assert over <= 1, (b, h, over)
             fin = np.isfinite(wl)

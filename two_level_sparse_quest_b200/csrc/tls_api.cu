@@ -750,6 +750,7 @@ tls_status tls_kv4_attn_decode(const tls_shape *s, const void *q, const void *ca
   a.out = out;
   a.lse = lse_out;
   a.part = static_cast<float *>(ws);
+  a.err = tls::device_error_word();
   return cuda_status(tls::launch_kv4_attention(a, static_cast<cudaStream_t>(stream)), "kv4_attention launch");
 }
 

@@ -201,6 +201,7 @@ struct Kv4AttnArgs {
   void *out;
   float *lse;
   float *part;
+  int *err;
   int batch, n_q_heads, n_kv_heads, d, block_size, n_blocks_max, max_ctx, k_t, out_dtype;
   float scale_log2;
   int num_sms;

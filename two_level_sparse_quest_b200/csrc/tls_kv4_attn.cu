@@ -22,18 +22,21 @@
 // codes, a nibble of each token in a byte, before they are widened.
 //
 // Numerics: K and V are exact in fp16; q is (tls_kv4.cuh, q_norm); sums are
-// fp32.  P is 2^(s - m + 14), below 2^15, as fp16 high and low parts (22
-// bits; what falls below 2^-38 of the largest weight is dropped): with one
-// part the fp32 output would be off by 1e-4.  m is a running reference that
-// moves only when a score exceeds it by more than one (log2).
+// fp32.  P is 2^(s - m + 14), at most 2^15, in fp16 (what falls below 2^-38 of
+// the largest weight is dropped); m is a running reference that moves only
+// when a score exceeds it by more than one (log2).  For an fp32 output P is
+// two fp16 parts, high and low (22 bits): with one it would be off by 1e-4.
+// A bf16 output takes one part, whose 2^-12 per weight is an eighth of the
+// output's own rounding and averages out over the tokens; the sum l is of the
+// unrounded weights in both.
 //
 // Work split: a unit is one group (or 16 of its heads).  A thread-block
-// cluster of up to 8 CTAs takes a unit (or one of its n_split parts), every
-// warp 32-token tiles in turn through its own cp.async ring; the warps' and
-// then the CTAs' partial (m, l, O) are joined in shared memory, the CTAs' over
-// distributed shared memory, so that one launch does the whole step.  With
-// too few units to fill the GPU (n_split > 1) the clusters leave partials in
-// the workspace and a second launch joins them.
+// cluster of up to 8 CTAs takes a unit, every warp 32-token tiles in turn
+// through its own ring in shared memory; the warps' and then the CTAs' partial
+// (m, l, O) are joined in shared memory, the CTAs' over distributed shared
+// memory, so that one launch does the whole step.  Long calls are cut into
+// parts that leave their partials in the workspace for a second launch
+// (kv4_plan).
 #include <algorithm>
 
 #include "tls_internal.h"
@@ -47,27 +50,37 @@ constexpr int kTile = 32;   // tokens per ring stage
 constexpr int kWarps = 8;   // per CTA
 constexpr int kRing = 3;
 constexpr int kMaxCluster = 8;
-constexpr float kPShift = 14.f;  // P is scaled by 2^14
+constexpr int kMaxSplit = 64;
+constexpr float kPShift = 14.f;     // P is scaled by 2^14
+constexpr float kNoMax = -3e38f;    // a warp's m before its first token: finite, so that a masked score stays -inf
 
 template <int D, int NT>
 struct Kv4Smem {
   using R = Kv4Rec<D>;
   static constexpr int kStage = kTile * R::kBytes;
-  static constexpr int kWarpBytes = kRing * kStage;
-  static constexpr int kSmem = kWarps * kWarpBytes;
   // A warp's partial O [8 NT heads][D channels] overlays its ring.  Two words
   // of padding per lane group's channels and a head stride of 4 mod 16 keep
   // the 8-byte stores of a half warp in distinct banks.
   static constexpr int kCpl = D / 8;  // channels per lane group
   static constexpr int kHead = 8 * (kCpl + 2) + 4;
   static_assert(kHead % 16 == 4, "bank spread of the partial's heads");
-  static_assert(8 * NT * kHead * 4 <= kWarpBytes, "the partial fits the ring");
+  static constexpr int kPartial = 8 * NT * kHead * 4;
+  static constexpr int kWarpBytes = kRing * kStage > kPartial ? kRing * kStage : kPartial;
+  static constexpr int kSmem = kWarps * kWarpBytes;
+  static_assert(kWarpBytes % 16 == 0, "every ring starts on 16 bytes");
   static __device__ __forceinline__ int at(int head, int ch) { return head * kHead + ch + 2 * (ch / kCpl); }
 };
 
 template <int BYTES>
-__device__ __forceinline__ void cp_async_zfill(uint32_t dst, const void *src, bool ok) {
-  const int n = ok ? BYTES : 0;
+__device__ __forceinline__ void cp_async_chunk(uint32_t dst, const void *src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(dst), "l"(src) : "memory");
+}
+template <int BYTES>
+__device__ __forceinline__ void cp_async_chunk(uint32_t dst, const void *src, bool ok) {
+  const int n = ok ? BYTES : 0;  // 0 source bytes: zero-filled
   if constexpr (BYTES == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
   else
@@ -76,7 +89,7 @@ __device__ __forceinline__ void cp_async_zfill(uint32_t dst, const void *src, bo
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
   return r;
 }
 
@@ -92,17 +105,20 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
 // (rows 2c) collide in shared memory at d 128.
 __device__ __forceinline__ int row_token(int row) { return (0x57463120u >> (4 * row)) & 15; }
 
-template <int D, int NT, bool LIST, bool PAGED>
-__global__ void __launch_bounds__(kWarps * 32, 2) kv4_attn_kernel(Kv4AttnArgs a) {
+template <int D, int NT, bool LIST, bool PAGED, bool F32OUT>
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(Kv4AttnArgs a) {
   using R = Kv4Rec<D>;
   using L = Kv4Smem<D, NT>;
-  constexpr int KS = D / 16;   // MMA steps of S
   constexpr int OT = D / 16;   // 16-channel tiles of O
   constexpr int CW = D / 32;   // 32-bit words of K codes per lane and token
   constexpr int VW = D / 64;   // 32-bit words of V codes per lane and token
+  constexpr bool kBulk = !LIST && R::kBytes % 16 == 0;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float s_ml[kWarps][8 * NT][2];
   __shared__ float s_cta[8 * NT][2];
+  __shared__ uint4 s_q[NT][D / 32][32];
+  __shared__ float s_scale[8 * NT];
+  __shared__ uint64_t s_full[kWarps][kRing];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
   unsigned char *ring = smem + warp * L::kWarpBytes;
@@ -147,28 +163,63 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_attn_kernel(Kv4AttnArgs a)
     return (slot >= 0 && slot < a.n_slots) ? slot * a.block_size + (tok - blk * a.block_size) : -1;
   };
 
-  // Ring: copies of one stage are 288 chunks of D / 8 bytes, nine per lane,
-  // neighbouring lanes on neighbouring bytes.
+  // The ring.  Neighbouring tokens at d 128 (a record is a multiple of 16
+  // bytes) come with one bulk copy a stage, counted by the stage's mbarrier;
+  // tokens past the end get zero scales, so that stale bytes stay finite.
+  // Listed tokens come with cp.async, nine chunks of d / 8 bytes a record,
+  // zero-filled: eight lanes bring a record's first eight chunks, then every
+  // lane its own record's ninth.  (One bulk copy per listed record was slower:
+  // 24.0 us against 20.4 for 8 x 96k, 4096 tokens.)
   uint32_t valid[kRing];  // valid tokens of the stages in flight, oldest first
 #pragma unroll
   for (int s = 0; s < kRing; ++s) valid[s] = 0;
-  int row_next = row_of(t_issue), stage_issue = 0;
+  // rows of the next two tiles: their ids are on the way while earlier tiles are copied and computed
+  int row_next = row_of(t_issue), row_after = row_of(t_issue + stride), stage_issue = 0;
+  if constexpr (kBulk) {
+    if (lane == 0) {
+#pragma unroll
+      for (int s = 0; s < kRing; ++s) mbarrier_init(&s_full[warp][s], 1);
+      mbarrier_init_fence();
+    }
+    __syncwarp();
+  }
   auto issue = [&]() -> uint32_t {
     const int row = row_next;
     const uint32_t mask = __ballot_sync(0xffffffffu, row >= 0);
     if (mask != 0u) {
-      const uint32_t dst = ring_s + stage_issue * L::kStage + lane * R::kChunk;
+      if constexpr (kBulk) {
+        uint64_t *bar = &s_full[warp][stage_issue];
+        if (lane == 0) mbarrier_expect_tx(bar, __popc(mask) * R::kBytes);
+        if (lane == 0)
+          bulk_load(ring + stage_issue * L::kStage, base + static_cast<size_t>(row) * R::kBytes, __popc(mask) * R::kBytes, bar);
+        if (mask != 0xffffffffu && row < 0)  // the last stage of all: nothing is copied over these zeros
+          *reinterpret_cast<uint4 *>(ring + stage_issue * L::kStage + lane * R::kBytes + R::kKS) = make_uint4(0u, 0u, 0u, 0u);
+      } else {
+        constexpr int CB = R::kChunk;
+        const uint32_t dst = ring_s + stage_issue * L::kStage;
+        const unsigned char *src = base + (lane & 7) * CB;
+        if (mask == 0xffffffffu) {
 #pragma unroll
-      for (int i = 0; i < 9; ++i) {
-        const int idx = i * 32 + lane;
-        const int tk = (idx * 57) >> 9;  // idx / 9 for idx < 288
-        const int rw = __shfl_sync(0xffffffffu, row, tk);
-        const long long off = static_cast<long long>(rw - tk) * R::kBytes + idx * R::kChunk;
-        cp_async_zfill<R::kChunk>(dst + i * 32 * R::kChunk, base + (rw >= 0 ? off : 0), rw >= 0);
+          for (int i = 0; i < 8; ++i) {
+            const long long u = __shfl_sync(0xffffffffu, row, 4 * i + (lane >> 3));
+            cp_async_chunk<CB>(dst + (4 * i + (lane >> 3)) * R::kBytes + (lane & 7) * CB, src + u * R::kBytes);
+          }
+          cp_async_chunk<CB>(dst + lane * R::kBytes + 8 * CB, base + static_cast<long long>(row) * R::kBytes + 8 * CB);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const long long u = __shfl_sync(0xffffffffu, row, 4 * i + (lane >> 3));
+            cp_async_chunk<CB>(dst + (4 * i + (lane >> 3)) * R::kBytes + (lane & 7) * CB,
+                               u >= 0 ? src + u * R::kBytes : base, u >= 0);
+          }
+          cp_async_chunk<CB>(dst + lane * R::kBytes + 8 * CB,
+                             row >= 0 ? base + static_cast<long long>(row) * R::kBytes + 8 * CB : base, row >= 0);
+        }
       }
     }
     t_issue += stride;
-    row_next = row_of(t_issue);
+    row_next = row_after;
+    row_after = row_of(t_issue + stride);
     if (++stage_issue == kRing) stage_issue = 0;
     return mask;
   };
@@ -176,16 +227,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_attn_kernel(Kv4AttnArgs a)
 #pragma unroll
   for (int s = 0; s < kRing - 1; ++s) {
     valid[s + 1] = issue();
-    cp_async_commit();
+    if constexpr (!kBulk) cp_async_commit();
   }
 
-  // Queries: B fragments of S^T = K q^T.  Lane (g, c) holds head 8 nt + g's
-  // channels c D/4 .. + D/4 - 1, four per MMA step.
-  uint32_t qb[NT][KS][2];
-  float sl[NT][2];  // score scale of this lane's columns (heads 8 nt + 2c, + 1)
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int h = nt * 8 + g;
+  // Queries: B fragments of S^T = K q^T in shared memory, two MMA steps a
+  // read.  Lane (g, c) holds head 8 nt + g's channels c D/4 .. + D/4 - 1, four
+  // per step.
+  if (warp < NT) {
+    const int h = warp * 8 + g;
     uint32_t w[D / 8];
     uint32_t ex = 0;
     const uint4 *qp = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) +
@@ -205,12 +254,17 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_attn_kernel(Kv4AttnArgs a)
     float undo;
     const float mult = q_norm(ex, &undo);
 #pragma unroll
-    for (int j = 0; j < KS; ++j) {
-      qb[nt][j][0] = q_to_f16(w[2 * j], mult);
-      qb[nt][j][1] = q_to_f16(w[2 * j + 1], mult);
-    }
-    sl[nt][0] = a.scale_log2 * __shfl_sync(0xffffffffu, undo, 8 * c);
-    sl[nt][1] = a.scale_log2 * __shfl_sync(0xffffffffu, undo, 8 * c + 4);
+    for (int i = 0; i < D / 32; ++i)
+      s_q[warp][i][lane] = make_uint4(q_to_f16(w[4 * i], mult), q_to_f16(w[4 * i + 1], mult),
+                                      q_to_f16(w[4 * i + 2], mult), q_to_f16(w[4 * i + 3], mult));
+    if (c == 0) s_scale[h] = a.scale_log2 * undo;
+  }
+  __syncthreads();
+  float sl[NT][2];  // score scale of this lane's columns (heads 8 nt + 2c, + 1)
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    sl[nt][0] = s_scale[nt * 8 + 2 * c];
+    sl[nt][1] = s_scale[nt * 8 + 2 * c + 1];
   }
 
   float o[NT][OT][4];
@@ -221,7 +275,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_attn_kernel(Kv4AttnArgs a)
     for (int j = 0; j < OT; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[nt][j][e] = 0.f;
-    m[nt][0] = m[nt][1] = -INFINITY;
+    m[nt][0] = m[nt][1] = kNoMax;
     l[nt][0] = l[nt][1] = 0.f;
   }
 
@@ -229,24 +283,39 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_attn_kernel(Kv4AttnArgs a)
   const int vtok0 = 2 * row_token(2 * c), vtok1 = 2 * row_token(2 * c + 1);
 
   int st = 0;
+  uint32_t phases = 0;  // mbarrier parity of each stage
+  bool alive = true;
   for (int it = 0; it < my_tiles; ++it) {
 #pragma unroll
     for (int s = 0; s + 1 < kRing; ++s) valid[s] = valid[s + 1];
-    valid[kRing - 1] = issue();
-    cp_async_commit();
-    cp_async_wait<kRing - 1>();
-    __syncwarp();
+    valid[kRing - 1] = alive ? issue() : 0u;
+    if constexpr (!kBulk) {
+      cp_async_commit();
+      cp_async_wait<kRing - 1>();
+      __syncwarp();
+    }
     const uint32_t vm = valid[0];
-    if (vm != 0u) {
+    if constexpr (kBulk) {
+      if (vm != 0u) {  // a wait that gives up (which a correct run never sees): no further copies, the result is undefined
+        if (!mbarrier_wait(&s_full[warp][st], (phases >> st) & 1u)) alive = false;
+        phases ^= 1u << st;
+        if (!__all_sync(0xffffffffu, alive)) {
+          alive = false;
+          if (lane == 0 && a.err) atomicOr(a.err, kErrAttnWait);
+        }
+      }
+    }
+    if (vm != 0u && alive) {
       const unsigned char *S = ring + st * L::kStage;
-      float s[2][NT][4];  // [half]: rows g, g + 8 of heads 2c, 2c + 1
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll NT == 1 ? 2 : 1
+      for (int hf = 0; hf < 2; ++hf, S += R::kBytes) {  // even tokens of the stage, then odd ones
+        // ---- S^T = K q^T: rows g, g + 8 of heads 2c, 2c + 1
+        float s[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[hf][nt][e] = 0.f;
-        const unsigned char *k0 = S + (ktok + hf) * R::kBytes, *k1 = k0 + 16 * R::kBytes;
+          for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+        const unsigned char *k0 = S + ktok * R::kBytes, *k1 = k0 + 16 * R::kBytes;
         uint32_t w0[CW], w1[CW], sc0, sc1;
         if constexpr (D == 128) {
           *reinterpret_cast<uint4 *>(w0) = *reinterpret_cast<const uint4 *>(k0 + 16 * c);
@@ -274,68 +343,74 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_attn_kernel(Kv4AttnArgs a)
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma_f16(s[hf][nt], x[0], y[0], x[1], y[1], qb[nt][2 * w][0], qb[nt][2 * w][1]);
-            mma_f16(s[hf][nt], x[2], y[2], x[3], y[3], qb[nt][2 * w + 1][0], qb[nt][2 * w + 1][1]);
+            const uint4 qv = s_q[nt][w][lane];
+            mma_f16(s[nt], x[0], y[0], x[1], y[1], qv.x, qv.y);
+            mma_f16(s[nt], x[2], y[2], x[3], y[3], qv.z, qv.w);
           }
         }
-      }
-      // ---- online softmax in the log2 domain
-      bool over = false;
+        // ---- online softmax in the log2 domain: t = score - m + 14
+        if (vm != 0xffffffffu) {
+          const bool ok0 = (vm >> (ktok + hf)) & 1u, ok1 = (vm >> (ktok + 16 + hf)) & 1u;
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const bool ok0 = (vm >> (ktok + hf)) & 1u, ok1 = (vm >> (ktok + 16 + hf)) & 1u;
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!(e < 2 ? ok0 : ok1)) s[nt][e] = -INFINITY;
+        }
+        float top = -INFINITY;
+        float t[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            s[hf][nt][e] = (e < 2 ? ok0 : ok1) ? s[hf][nt][e] * sl[nt][e & 1] : -INFINITY;
-            over |= s[hf][nt][e] > m[nt][e & 1] + 1.f;
+            t[nt][e] = fmaf(s[nt][e], sl[nt][e & 1], kPShift - m[nt][e & 1]);
+            top = fmaxf(top, t[nt][e]);
           }
-      }
-      if (__any_sync(0xffffffffu, over)) {
+        if (__any_sync(0xffffffffu, top > kPShift + 1.f)) {  // some score exceeds its head's m by more than one
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float mx = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            if (mx > m[nt][e]) {
-              const float alpha = ex2(m[nt][e] - mx);  // 0 for the first tokens
-              m[nt][e] = mx;
-              l[nt][e] *= alpha;
+            for (int e = 0; e < 2; ++e) {
+              float mx = fmaxf(s[nt][e], s[nt][e + 2]) * sl[nt][e];
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+              if (mx > m[nt][e]) {
+                const float alpha = ex2(m[nt][e] - mx);  // 0 for the first tokens
+                m[nt][e] = mx;
+                l[nt][e] *= alpha;
 #pragma unroll
-              for (int j = 0; j < OT; ++j) {
-                o[nt][j][e] *= alpha;
-                o[nt][j][e + 2] *= alpha;
+                for (int j = 0; j < OT; ++j) {
+                  o[nt][j][e] *= alpha;
+                  o[nt][j][e + 2] *= alpha;
+                }
+                t[nt][e] = fmaf(s[nt][e], sl[nt][e], kPShift - mx);
+                t[nt][e + 2] = fmaf(s[nt][e + 2], sl[nt][e], kPShift - mx);
               }
             }
-          }
-      }
-      // ---- O^T += V^T P^T
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
+        }
+        // ---- O^T += V^T P^T
         uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float p[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float mm = m[nt][e & 1];
-            p[e] = ex2(s[hf][nt][e] - (mm == -INFINITY ? 0.f : mm) + kPShift);
+            p[e] = ex2(t[nt][e]);
             l[nt][e & 1] += p[e];
           }
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             const __half2 hi = __floats2half2_rn(p[2 * r], p[2 * r + 1]);
-            const float2 hf2 = __half22float2(hi);
-            const __half2 lo = __floats2half2_rn(p[2 * r] - hf2.x, p[2 * r + 1] - hf2.y);
             ph[nt][r] = movmatrix(*reinterpret_cast<const uint32_t *>(&hi));
-            pl[nt][r] = movmatrix(*reinterpret_cast<const uint32_t *>(&lo));
+            if constexpr (F32OUT) {
+              const float2 hf2 = __half22float2(hi);
+              const __half2 lo = __floats2half2_rn(p[2 * r] - hf2.x, p[2 * r + 1] - hf2.y);
+              pl[nt][r] = movmatrix(*reinterpret_cast<const uint32_t *>(&lo));
+            }
           }
         }
-        const unsigned char *v0 = S + (vtok0 + hf) * R::kBytes, *v1 = S + (vtok1 + hf) * R::kBytes;
+        const unsigned char *v0 = S + vtok0 * R::kBytes, *v1 = S + vtok1 * R::kBytes;
         constexpr int V8 = 16 * R::kBytes;  // rows 8 more: 16 tokens on
         uint32_t w[4][VW], sc[2];
 #pragma unroll
@@ -368,7 +443,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_attn_kernel(Kv4AttnArgs a)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               mma_f16(o[nt][4 * q + j], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
-              mma_f16(o[nt][4 * q + j], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+              if constexpr (F32OUT) mma_f16(o[nt][4 * q + j], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
             }
           }
         }
@@ -377,7 +452,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_attn_kernel(Kv4AttnArgs a)
     __syncwarp();
     if (++st == kRing) st = 0;
   }
-  cp_async_wait<0>();
+  if constexpr (!kBulk) cp_async_wait<0>();
   __syncwarp();
 
   // ---- the warp's partial into its own ring
@@ -392,7 +467,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_attn_kernel(Kv4AttnArgs a)
       t += __shfl_xor_sync(0xffffffffu, t, 16);
       const int h = nt * 8 + 2 * c + e;
       if (g == 0) {
-        s_ml[warp][h][0] = m[nt][e];
+        s_ml[warp][h][0] = m[nt][e] == kNoMax ? -INFINITY : m[nt][e];
         s_ml[warp][h][1] = t;
       }
 #pragma unroll
@@ -482,27 +557,62 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_attn_kernel(Kv4AttnArgs a)
   }
 }
 
-// Joins the n_split partials of each unit: one thread per (head, channel).
+// Joins the n_split partials of one (unit, head): eight groups of D threads
+// take every eighth part, the groups are joined in shared memory.
+constexpr int kMergeGroups = 8;
 template <int D>
-__global__ void __launch_bounds__(128) kv4_merge_kernel(Kv4AttnArgs a) {
+__global__ void __launch_bounds__(kMergeGroups * D) kv4_merge_kernel(Kv4AttnArgs a) {
+  __shared__ float s_o[kMergeGroups][D], s_m[kMergeGroups], s_l[kMergeGroups];
   grid_dependency_wait();
-  const int unit = blockIdx.y;
-  const int i = blockIdx.x * 128 + threadIdx.x;
   const int HG = a.head_chunk;
-  if (i >= HG * D) return;
-  const int h = i / D, ch = i % D;
+  const int unit = blockIdx.x / HG, h = blockIdx.x % HG;
+  const int ch = threadIdx.x % D, grp = threadIdx.x / D;
   const size_t n_units = static_cast<size_t>(a.batch) * a.n_kv_heads * a.n_head_chunks;
   const float *ml = a.part + static_cast<size_t>(unit) * a.n_split * HG * 2 + 2 * h;
-  const float *po = a.part + n_units * a.n_split * HG * 2 + static_cast<size_t>(unit) * a.n_split * HG * D + i;
-  float M = -INFINITY;
-  for (int p = 0; p < a.n_split; ++p) M = fmaxf(M, ml[static_cast<size_t>(p) * HG * 2]);
+  const float *po = a.part + n_units * a.n_split * HG * 2 + static_cast<size_t>(unit) * a.n_split * HG * D + h * D + ch;
+  constexpr int U = 8;  // parts in flight
+  float M = -INFINITY, ls = 0.f, acc = 0.f;
+  for (int p0 = grp; p0 < a.n_split; p0 += U * kMergeGroups) {
+    float mv[U], lv[U], ov[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int p = p0 + u * kMergeGroups;
+      const bool ok = p < a.n_split;
+      mv[u] = ok ? ml[static_cast<size_t>(p) * HG * 2] : -INFINITY;
+      lv[u] = ok ? ml[static_cast<size_t>(p) * HG * 2 + 1] : 0.f;
+      ov[u] = ok ? po[static_cast<size_t>(p) * HG * D] : 0.f;
+    }
+    float Mn = M;
+#pragma unroll
+    for (int u = 0; u < U; ++u) Mn = fmaxf(Mn, mv[u]);
+    const float Mu = Mn == -INFINITY ? 0.f : Mn;
+    const float f0 = ex2(M - Mu);
+    ls *= f0;
+    acc *= f0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float f = ex2(mv[u] - Mu);
+      ls = fmaf(f, lv[u], ls);
+      acc = fmaf(f, ov[u], acc);
+    }
+    M = Mn;
+  }
+  s_o[grp][ch] = acc;
+  if (ch == 0) {
+    s_m[grp] = M;
+    s_l[grp] = ls;
+  }
+  __syncthreads();
+  if (grp != 0) return;
+#pragma unroll
+  for (int i = 0; i < kMergeGroups; ++i) M = fmaxf(M, s_m[i]);
   const float Mu = M == -INFINITY ? 0.f : M;
-  float ls = 0.f, acc = 0.f;
-#pragma unroll 8
-  for (int p = 0; p < a.n_split; ++p) {
-    const float f = ex2(ml[static_cast<size_t>(p) * HG * 2] - Mu);
-    ls = fmaf(f, ml[static_cast<size_t>(p) * HG * 2 + 1], ls);
-    acc = fmaf(f, po[static_cast<size_t>(p) * HG * D], acc);
+  ls = acc = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMergeGroups; ++i) {
+    const float f = ex2(s_m[i] - Mu);
+    ls = fmaf(f, s_l[i], ls);
+    acc = fmaf(f, s_o[i][ch], acc);
   }
   const int group = unit / a.n_head_chunks, hc = unit % a.n_head_chunks;
   const int b = group / a.n_kv_heads, gk = group % a.n_kv_heads;
@@ -513,28 +623,47 @@ __global__ void __launch_bounds__(128) kv4_merge_kernel(Kv4AttnArgs a) {
   if (a.lse && ch == 0) a.lse[head] = ls == 0.f ? -INFINITY : (M + (log2f(ls) - kPShift)) * 0.69314718055994531f;
 }
 
-// How a call is cut: heads per unit, CTAs per cluster, clusters per unit.
+// How a call is cut: heads per unit, and either CTAs per cluster or parts per
+// unit (joined by a second launch), whichever this estimate in tenths of a
+// microsecond (fitted at d 128, 4 heads) finds cheaper.  A warp takes 1.9 us
+// for a tile when two CTAs share an SM and 1.1 us alone; a wave of CTAs costs
+// 3.5 us around its tiles, a cluster 1 us, the second launch 3.  Measured:
+// 64 units of 4096 tokens 19.8 us with clusters of 4 (one wave), 22.0 with 2,
+// 25.5 with 8 (two waves), 27 as 9 parts; 64 units of 98304 tokens 172 us as 9
+// parts (two full waves), 184 with clusters of 4, 211 with 8.
 void kv4_plan(Kv4AttnArgs &a, int n_max) {
   const int G = a.n_q_heads / a.n_kv_heads;
   a.head_chunk = std::min(G, 16);
   a.n_head_chunks = G / a.head_chunk;
   const long long units = static_cast<long long>(a.batch) * a.n_kv_heads * a.n_head_chunks;
-  const int sms = a.num_sms > 0 ? a.num_sms : 148;
-  const long long slots = 2LL * sms;                               // CTAs resident at once
-  const long long tiles = (n_max + kTile - 1) / kTile;             // of one unit
-  const long long most = (tiles + kWarps - 1) / kWarps;            // CTAs that still have a tile for every warp
-  int cs = 1;
-  while (cs < kMaxCluster && cs * 2 <= most && units * cs < slots) cs *= 2;
-  a.cluster = cs;
-  a.n_split = 1;
-  if (cs == kMaxCluster && units * cs * 2 <= slots)
-    a.n_split = static_cast<int>(std::min<long long>(slots / (units * cs), std::max<long long>(1, most / cs)));
+  const long long sms = a.num_sms > 0 ? a.num_sms : 148;
+  const long long resident = a.head_chunk > 8 ? sms : 2 * sms;  // 16 heads: one CTA an SM (registers)
+  const long long tiles = std::max<long long>(1, (n_max + kTile - 1) / kTile);  // of one unit
+  a.cluster = a.n_split = 1;
+  long long best = -1;
+  auto consider = [&](int cluster, int n_split) {
+    const long long per_unit = static_cast<long long>(cluster) * n_split, ctas = units * per_unit;
+    const long long rounds = (tiles + per_unit * kWarps - 1) / (per_unit * kWarps);
+    // clusters of 4 and 8 do not fill every GPC: 7/8 and 13/16 of the places (at one CTA an SM 132 and 120 of 148 run at once)
+    const long long places = cluster == 8 ? resident * 13 / 16 : cluster == 4 ? resident * 7 / 8 : resident;
+    const long long waves = (ctas + places - 1) / places;
+    const long long cost = waves * (35 + rounds * (ctas <= sms ? 11 : 19)) + (cluster > 1 ? 10 : 0) + (n_split > 1 ? 30 : 0);
+    if (best < 0 || cost < best) {
+      best = cost;
+      a.cluster = cluster;
+      a.n_split = n_split;
+    }
+  };
+  const long long most = (tiles + kWarps - 1) / kWarps;  // CTAs of a unit that still have a tile for every warp
+  for (int c = 1; c <= kMaxCluster && (c == 1 || c <= most); c *= 2) consider(c, 1);
+  for (int c : {1, kMaxCluster})
+    for (int p = 2; p <= kMaxSplit && c * p <= most; ++p) consider(c, p);
 }
 
-template <int D, int NT, bool LIST, bool PAGED>
+template <int D, int NT, bool LIST, bool PAGED, bool F32OUT>
 cudaError_t run(const Kv4AttnArgs &a, cudaStream_t st) {
   using L = Kv4Smem<D, NT>;
-  auto kern = kv4_attn_kernel<D, NT, LIST, PAGED>;
+  auto kern = kv4_attn_kernel<D, NT, LIST, PAGED, F32OUT>;
   static bool configured[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -547,10 +676,14 @@ cudaError_t run(const Kv4AttnArgs &a, cudaStream_t st) {
   return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(ctas)), dim3(kWarps * 32), L::kSmem, st, a.cluster, a);
 }
 
+template <int D, int NT, bool F32OUT>
+cudaError_t dispatch(const Kv4AttnArgs &a, cudaStream_t st) {
+  if (!a.token_idx) return run<D, NT, false, false, F32OUT>(a, st);
+  return a.slot_of_block ? run<D, NT, true, true, F32OUT>(a, st) : run<D, NT, true, false, F32OUT>(a, st);
+}
 template <int D, int NT>
 cudaError_t dispatch(const Kv4AttnArgs &a, cudaStream_t st) {
-  if (!a.token_idx) return run<D, NT, false, false>(a, st);
-  return a.slot_of_block ? run<D, NT, true, true>(a, st) : run<D, NT, true, false>(a, st);
+  return a.out_dtype == 1 ? dispatch<D, NT, false>(a, st) : dispatch<D, NT, true>(a, st);
 }
 
 }  // namespace
@@ -573,9 +706,9 @@ cudaError_t launch_kv4_attention(Kv4AttnArgs a, cudaStream_t st) {
   if (a.d == 128) e = a.head_chunk > 8 ? dispatch<128, 2>(a, st) : dispatch<128, 1>(a, st);
   else e = a.head_chunk > 8 ? dispatch<64, 2>(a, st) : dispatch<64, 1>(a, st);
   if (e != cudaSuccess || a.n_split == 1) return e;
-  const dim3 grid((a.head_chunk * a.d + 127) / 128, a.batch * a.n_kv_heads * a.n_head_chunks);
-  if (a.d == 128) return launch_pdl(kv4_merge_kernel<128>, grid, dim3(128), 0, st, a);
-  return launch_pdl(kv4_merge_kernel<64>, grid, dim3(128), 0, st, a);
+  const dim3 grid(a.batch * a.n_q_heads);  // units times their heads
+  if (a.d == 128) return launch_pdl(kv4_merge_kernel<128>, grid, dim3(kMergeGroups * 128), 0, st, a);
+  return launch_pdl(kv4_merge_kernel<64>, grid, dim3(kMergeGroups * 64), 0, st, a);
 }
 
 }  // namespace tls

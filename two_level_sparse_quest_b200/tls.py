@@ -132,9 +132,27 @@ def _dptr(x):
     """Pointer of an argument the kernels read or write on the device: a CUDA
     tensor (a host tensor is refused here, before it could reach a kernel) or
     a raw integer pointer, passed as is."""
-    if isinstance(x, torch.Tensor) and x.device.type != "cuda":
-        raise ValueError("expected a CUDA tensor (the kernels address device memory)")
+    if isinstance(x, torch.Tensor):
+        if not x.is_cuda:
+            raise ValueError("expected a CUDA tensor (the kernels address device memory)")
+        if not x.is_contiguous():
+            raise ValueError("tensor must be contiguous")
+        return x.data_ptr()
     return _ptr(x)
+
+
+def _dptrs(*xs):
+    """_dptr of several arguments, whose tensors must lie on the current device
+    (the one that the call launches on)."""
+    dev, out = None, []
+    for x in xs:
+        out.append(_dptr(x))
+        if isinstance(x, torch.Tensor):
+            if dev is None:
+                dev = torch.cuda.current_device()
+            if x.get_device() != dev:
+                raise ValueError(f"tensor on cuda:{x.get_device()}, but the current device is cuda:{dev}")
+    return out
 
 
 def _hptr(x):
@@ -146,6 +164,9 @@ def _hptr(x):
 
 def _stream(stream):
     if stream is None:
+        # the handle alone: a torch.cuda.Stream object costs 3 us a call
+        if torch.cuda.is_initialized():
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -157,7 +178,7 @@ def _ws(ws):
         return None, 0
     if isinstance(ws, tuple):
         return ws
-    return _dptr(ws), ws.numel() * ws.element_size()
+    return _dptr(ws), ws.nbytes
 
 
 def _check(st: int, name: str):
@@ -285,43 +306,43 @@ def tls_kv4_append(shape, K, V, old_lens, new_lens, row_stride, cache, label_idx
                    stream=None):
     """Quantises the rows of tokens [old_lens, new_lens) into the 4-bit cache; with meta / slab given, brings the
     block summary and the label slab up to date with them."""
-    _check(_lib.tls_kv4_append(ctypes.byref(shape), _dptr(K), _dptr(V), _dptr(old_lens), _dptr(new_lens),
-                               int(row_stride), _dptr(label_idx), _dptr(cache), _dptr(meta), _dptr(slab),
-                               _stream(stream)), "tls_kv4_append")
+    pK, pV, po, pn, pl, pc, pm, ps = _dptrs(K, V, old_lens, new_lens, label_idx, cache, meta, slab)
+    _check(_lib.tls_kv4_append(ctypes.byref(shape), pK, pV, po, pn, int(row_stride), pl, pc, pm, ps, _stream(stream)),
+           "tls_kv4_append")
 
 
 def tls_kv4_read(shape, cache, old_lens, new_lens, row_stride, K_out=None, V_out=None, stream=None):
     """The stored values of tokens [old_lens, new_lens) as bf16 rows."""
-    _check(_lib.tls_kv4_read(ctypes.byref(shape), _dptr(cache), _dptr(old_lens), _dptr(new_lens), int(row_stride),
-                             _dptr(K_out), _dptr(V_out), _stream(stream)), "tls_kv4_read")
+    pc, po, pn, pK, pV = _dptrs(cache, old_lens, new_lens, K_out, V_out)
+    _check(_lib.tls_kv4_read(ctypes.byref(shape), pc, po, pn, int(row_stride), pK, pV, _stream(stream)),
+           "tls_kv4_read")
 
 
 def tls_kv4_attn_decode(shape, q, cache, out, lse_out=None, token_idx=None, seq_lens=None, slot_of_block=None,
                         n_slots=0, ws=None, stream=None):
     """Attention over a 4-bit cache: the tokens of token_idx, or without it every token below seq_lens."""
     wp, wb = _ws(ws)
-    _check(_lib.tls_kv4_attn_decode(ctypes.byref(shape), _dptr(q), _dptr(cache), _dptr(token_idx), _dptr(seq_lens),
-                                    _dptr(slot_of_block), int(n_slots), _dptr(out), _dptr(lse_out), wp, wb,
+    pq, pc, pt, pn, ps, po, pl = _dptrs(q, cache, token_idx, seq_lens, slot_of_block, out, lse_out)
+    _check(_lib.tls_kv4_attn_decode(ctypes.byref(shape), pq, pc, pt, pn, ps, int(n_slots), po, pl, wp, wb,
                                     _stream(stream)), "tls_kv4_attn_decode")
 
 
 def tls_accum_weights(shape, q, K, lse, weights, token_idx=None, seq_lens=None, stream=None):
     """Adds the step's attention weights, summed over each group's heads, to one fp32 number per token."""
-    _check(_lib.tls_accum_weights(ctypes.byref(shape), _dptr(q), _dptr(K), _dptr(token_idx), _dptr(seq_lens),
-                                  _dptr(lse), _dptr(weights), _stream(stream)), "tls_accum_weights")
+    _check(_lib.tls_accum_weights(ctypes.byref(shape), *_dptrs(q, K, token_idx, seq_lens, lse, weights),
+                                  _stream(stream)), "tls_accum_weights")
 
 
 def tls_kv4_accum_weights(shape, q, cache, lse, weights, token_idx=None, seq_lens=None, stream=None):
     """tls_accum_weights over the keys of a 4-bit cache."""
-    _check(_lib.tls_kv4_accum_weights(ctypes.byref(shape), _dptr(q), _dptr(cache), _dptr(token_idx),
-                                      _dptr(seq_lens), _dptr(lse), _dptr(weights), _stream(stream)),
-           "tls_kv4_accum_weights")
+    _check(_lib.tls_kv4_accum_weights(ctypes.byref(shape), *_dptrs(q, cache, token_idx, seq_lens, lse, weights),
+                                      _stream(stream)), "tls_kv4_accum_weights")
 
 
 def tls_evict_select(shape, budget, n_sink, n_recent, weights, seq_lens, keep_idx_out, new_lens_out, stream=None):
     """The tokens that stay: the first n_sink, the last n_recent, the rest by weight, `budget` in all."""
-    _check(_lib.tls_evict_select(ctypes.byref(shape), int(budget), int(n_sink), int(n_recent), _dptr(weights),
-                                 _dptr(seq_lens), _dptr(keep_idx_out), _dptr(new_lens_out), _stream(stream)),
+    _check(_lib.tls_evict_select(ctypes.byref(shape), int(budget), int(n_sink), int(n_recent),
+                                 *_dptrs(weights, seq_lens, keep_idx_out, new_lens_out), _stream(stream)),
            "tls_evict_select")
 
 
@@ -334,15 +355,15 @@ def tls_evict_compact(shape, budget, keep_idx, seq_lens, rows, weights=None, str
             want = (shape.batch, shape.n_kv_heads, shape.max_ctx)
             if tuple(x.shape[:3]) != want:
                 raise ValueError(f"rows tensors start with [B, H_kv, max_ctx] = {list(want)}, got {list(x.shape)}")
-            ptrs.append(_dptr(x))
+            ptrs.extend(_dptrs(x))
             sizes.append(math.prod(x.shape[3:]) * x.element_size())
         else:
             ptrs.append(x[0])
             sizes.append(int(x[1]))
     n = len(ptrs)
-    _check(_lib.tls_evict_compact(ctypes.byref(shape), int(budget), _dptr(keep_idx), _dptr(seq_lens), n,
-                                  (_P * max(n, 1))(*ptrs), (_i32 * max(n, 1))(*sizes), _dptr(weights),
-                                  _stream(stream)), "tls_evict_compact")
+    pk, pn, pw = _dptrs(keep_idx, seq_lens, weights)
+    _check(_lib.tls_evict_compact(ctypes.byref(shape), int(budget), pk, pn, n, (_P * max(n, 1))(*ptrs),
+                                  (_i32 * max(n, 1))(*sizes), pw, _stream(stream)), "tls_evict_compact")
 
 
 def tls_block_score_topk_noalloc(shape, q, meta, seq_lens, block_idx_out, stream=None):
