@@ -827,7 +827,7 @@ tls_status tls_evict_select(const tls_shape *s, int32_t budget, int32_t n_sink, 
   if (overlap(seq_lens, lens_bytes, new_lens_out, lens_bytes))  // other CTAs still read the old lengths
     return fail(TLS_ERR_INVALID_ARG, "new_lens_out overlaps seq_lens");
   const tls::EvictArgs a{weights, seq_lens, keep_idx_out, new_lens_out, s->batch, s->n_kv_heads,
-                         s->max_ctx, budget, n_sink, n_recent};
+                         s->max_ctx, budget, n_sink, n_recent, device_sms()};
   return cuda_status(tls::launch_evict_select(a, static_cast<cudaStream_t>(stream)), "evict_select launch");
 }
 

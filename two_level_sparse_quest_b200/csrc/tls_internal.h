@@ -229,7 +229,7 @@ struct EvictArgs {
   const float *weights;
   const int32_t *seq_lens;
   int32_t *keep_idx, *new_lens;
-  int batch, n_kv_heads, max_ctx, budget, n_sink, n_recent;
+  int batch, n_kv_heads, max_ctx, budget, n_sink, n_recent, num_sms;
 };
 cudaError_t launch_evict_select(const EvictArgs &a, cudaStream_t st);
 constexpr int kMaxEvictRows = 8;
