@@ -38,22 +38,55 @@ __device__ __forceinline__ float kv4_scale_value(int b) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(b << 7)));
 }
 
-// Scale byte of a group whose largest magnitude is amax (finite): amax / 6
-// rounded to nearest even.  Above 2^-14 the byte is the fp32 number's exponent
-// and top three mantissa bits; below, the scales are the multiples of 2^-17.
+// x / y for a y whose approximate reciprocal is r: one residual step leaves
+// the quotient within 2^-40, which rounds an exact one (the ties below) exactly.
+__device__ __forceinline__ float quotient(float x, float y, float r) {
+  const float q = x * r;
+  return fmaf(fmaf(-q, y, x), r, q);
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Scale byte of a group whose largest magnitude is amax (a finite bf16):
+// amax / 6 rounded to nearest even.  Above 2^-14 the byte is the fp32 number's
+// exponent and top three mantissa bits; below, the scales are the multiples of
+// 2^-17.  (amax has 8 significant bits: amax / 6 is a tie exactly, or further
+// from one than fp32's rounding.)
 __device__ __forceinline__ int kv4_scale_byte(float amax) {
-  const float s = __fdiv_rn(amax, 6.0f);
+  const float s = quotient(amax, 6.0f, 0.16666667f);
   if (s < 6.103515625e-05f) return __float2int_rn(s * 131072.0f);
   const uint32_t u = __float_as_uint(s);
   const int b = static_cast<int>((u + 0x7ffffu + ((u >> 20) & 1u)) >> 20) - (112 << 3);
   return min(b, kKv4MaxScale);
 }
 
-// Two fp32 -> one byte of e2m1 codes (x0 in the low nibble), nearest even, clamped to +-6.
-__device__ __forceinline__ uint32_t e2m1_pack(float x0, float x1) {
-  uint32_t r;
-  asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n cvt.u32.u8 %0, t;\n}\n" : "=r"(r) : "f"(x0), "f"(x1));
-  return r;
+// Eight bf16 (w[0..3]) over the scale s (reciprocal about r) -> eight e2m1
+// codes, nearest even, clamped to +-6, the first in the low nibble.
+__device__ __forceinline__ uint32_t e2m1_codes(const uint32_t (&w)[4], float s, float r) {
+  unsigned long long ns, rr;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(ns) : "f"(-s));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(rr) : "f"(r));
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // quotient(), two channels at once
+    unsigned long long x, t, e;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(bf16_lo(w[i])), "f"(bf16_hi(w[i])));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(x), "l"(rr));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(t), "l"(ns), "l"(x));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(t) : "l"(e), "l"(rr), "l"(t));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(q[2 * i]), "=f"(q[2 * i + 1]) : "l"(t));
+  }
+  uint32_t c;
+  asm("{\n .reg .b8 a, b, c, d;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      " mov.b32 %0, {a, b, c, d};\n}\n"
+      : "=r"(c)
+      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+  return c;
 }
 
 // The four bytes of w (eight codes) -> four fp16 pairs, low nibble first.
