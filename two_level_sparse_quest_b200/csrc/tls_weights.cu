@@ -30,8 +30,7 @@
 namespace tls {
 namespace {
 
-constexpr int kWThreads = 256;
-constexpr int kWWarps = kWThreads / 32;
+constexpr int kWThreads = 256;  // at most; fewer where the tiles do not reach every SM
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ int n_tokens(const WeightsArgs &a, int b) {
@@ -47,6 +46,7 @@ __device__ __forceinline__ int token_at(const WeightsArgs &a, int group, int j, 
 __device__ __forceinline__ void add_weight(float *p, float v) {
   asm volatile("red.global.add.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 // exp(x) for the sum; a head whose attention saw no token (lse = -inf) gives 0.
 __device__ __forceinline__ float weight_of(float s, float tau, float lse) {
   return lse == -INFINITY ? 0.f : ex2(fmaf(s, tau, -lse) * kLog2e);
@@ -65,9 +65,9 @@ __global__ void __launch_bounds__(kWThreads) weights_mma_kernel(WeightsArgs a) {
   using L = WeightsSmem<D, NT, KIND>;
   constexpr int KS = L::KS;
   extern __shared__ __align__(16) unsigned char smem[];
-  uint2 *qs = reinterpret_cast<uint2 *>(smem);                  // [NT][KS][32 lanes]
+  uint4 *qs = reinterpret_cast<uint4 *>(smem);                  // [NT][KS / 2][32 lanes]: two MMA steps a read
   float2 *hp = reinterpret_cast<float2 *>(smem + L::kQ);        // [8 NT] (tau, lse) of each head
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int g = lane >> 2, c = lane & 3;
   const int group = blockIdx.y, b = group / a.n_kv_heads, gk = group % a.n_kv_heads;
   const int G = a.n_q_heads / a.n_kv_heads;
@@ -75,20 +75,37 @@ __global__ void __launch_bounds__(kWThreads) weights_mma_kernel(WeightsArgs a) {
   grid_dependency_wait();
   const int n = n_tokens(a, b);
   const int tiles = (n + 15) / 16;
-  if (static_cast<int>(blockIdx.x) * kWWarps >= tiles) return;
+  if (static_cast<int>(blockIdx.x) * warps >= tiles) return;
 
-  // B fragments: lane (g, c) of block nt, step ks: four channels of head 8 nt + g
+  const int row_bytes = KIND == 1 ? 2 * D : Kv4Rec<KIND == 1 ? 128 : D>::kBytes;
+  const unsigned char *base =
+      static_cast<const unsigned char *>(a.keys) + static_cast<size_t>(group) * a.max_ctx * row_bytes;
+  float *out = a.weights + static_cast<size_t>(group) * a.max_ctx;
+  const int step = gridDim.x * warps;
+  int tile = blockIdx.x * warps + warp;
+  int t0 = token_at(a, group, tile * 16 + g, n), t1 = token_at(a, group, tile * 16 + 8 + g, n);
+
+  // B fragments: lane (g, c) of block nt: the 8 channels 32 i + 8 c of head 8 nt + g, steps 2 i and 2 i + 1
   if constexpr (KIND == 1) {
-    for (int i = threadIdx.x; i < NT * KS * 32; i += kWThreads) {
-      const int ln = i & 31, ks = (i >> 5) % KS, h = (i >> 5) / KS * 8 + (ln >> 2);
-      const int ch = 32 * (ks >> 1) + 8 * (ln & 3) + 4 * (ks & 1);
-      qs[i] = h < G ? *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.q) + (head0 + h) * D + ch)
-                    : make_uint2(0u, 0u);
+#pragma unroll 4
+    for (int i = threadIdx.x; i < NT * (KS / 2) * 32; i += blockDim.x) {
+      const int ln = i & 31, h = (i >> 5) / (KS / 2) * 8 + (ln >> 2), ch = 32 * ((i >> 5) % (KS / 2)) + 8 * (ln & 3);
+      cp_async16(qs + i, static_cast<const uint16_t *>(a.q) + (h < G ? (head0 + h) * D + ch : 0), h < G);
     }
-    for (int h = threadIdx.x; h < NT * 8; h += kWThreads)
+    cp_async_commit();
+    for (int h = threadIdx.x; h < NT * 8; h += blockDim.x)
       hp[h] = make_float2(a.scale, h < G ? a.lse[head0 + h] : -INFINITY);
+    if constexpr (D == 576) {  // long rows: on their way while the queries arrive
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (c + 4 * i < 9) {
+          prefetch_l2(base + static_cast<size_t>(max(t0, 0)) * row_bytes + (c + 4 * i) * 128);
+          prefetch_l2(base + static_cast<size_t>(max(t1, 0)) * row_bytes + (c + 4 * i) * 128);
+        }
+    }
+    cp_async_wait<0>();
   } else {
-    for (int h = warp; h < NT * 8; h += kWWarps) {  // one warp a head: its row as fp16, scaled by a power of two
+    for (int h = warp; h < NT * 8; h += warps) {  // one warp a head: its row as fp16, scaled by a power of two
       uint2 w = make_uint2(0u, 0u);
       const bool mine = lane * 4 < D;
       if (h < G && mine) w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.q) + (head0 + h) * D + 4 * lane);
@@ -96,21 +113,15 @@ __global__ void __launch_bounds__(kWThreads) weights_mma_kernel(WeightsArgs a) {
       float undo;
       const float mult = q_norm(ex, &undo);
       // channels 4 lane .. + 3: quarter lane / KS of the row, step lane % KS
+      const int ks = lane % KS;
       if (mine)
-        qs[((h >> 3) * KS + lane % KS) * 32 + (h & 7) * 4 + lane / KS] =
+        reinterpret_cast<uint2 *>(qs + ((h >> 3) * (KS / 2) + ks / 2) * 32 + (h & 7) * 4 + lane / KS)[ks & 1] =
             make_uint2(q_to_f16(w.x, mult), q_to_f16(w.y, mult));
       if (lane == 0) hp[h] = make_float2(a.scale * undo, h < G ? a.lse[head0 + h] : -INFINITY);
     }
   }
   __syncthreads();
 
-  const int row_bytes = KIND == 1 ? 2 * D : Kv4Rec<KIND == 1 ? 128 : D>::kBytes;
-  const unsigned char *base =
-      static_cast<const unsigned char *>(a.keys) + static_cast<size_t>(group) * a.max_ctx * row_bytes;
-  float *out = a.weights + static_cast<size_t>(group) * a.max_ctx;
-  const int step = gridDim.x * kWWarps;
-  int tile = blockIdx.x * kWWarps + warp;
-  int t0 = token_at(a, group, tile * 16 + g, n), t1 = token_at(a, group, tile * 16 + 8 + g, n);
   for (; tile < tiles; tile += step) {
     const unsigned char *r0 = base + static_cast<size_t>(max(t0, 0)) * row_bytes;
     const unsigned char *r1 = base + static_cast<size_t>(max(t1, 0)) * row_bytes;
@@ -136,9 +147,9 @@ __global__ void __launch_bounds__(kWThreads) weights_mma_kernel(WeightsArgs a) {
         for (int i = 0; i < U; ++i)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const uint2 b0 = qs[(nt * KS + 2 * (i0 + i)) * 32 + lane], b1 = qs[(nt * KS + 2 * (i0 + i) + 1) * 32 + lane];
-            mma_full(s[nt], x[i].x, y[i].x, x[i].y, y[i].y, b0.x, b0.y);
-            mma_full(s[nt], x[i].z, y[i].z, x[i].w, y[i].w, b1.x, b1.y);
+            const uint4 q = qs[(nt * (KS / 2) + i0 + i) * 32 + lane];
+            mma_full(s[nt], x[i].x, y[i].x, x[i].y, y[i].y, q.x, q.y);
+            mma_full(s[nt], x[i].z, y[i].z, x[i].w, y[i].w, q.z, q.w);
           }
       }
     } else {
@@ -170,9 +181,9 @@ __global__ void __launch_bounds__(kWThreads) weights_mma_kernel(WeightsArgs a) {
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const uint2 b0 = qs[(nt * KS + 2 * w) * 32 + lane], b1 = qs[(nt * KS + 2 * w + 1) * 32 + lane];
-          mma_f16(s[nt], x[0], y[0], x[1], y[1], b0.x, b0.y);
-          mma_f16(s[nt], x[2], y[2], x[3], y[3], b1.x, b1.y);
+          const uint4 q = qs[(nt * (KS / 2) + w) * 32 + lane];
+          mma_f16(s[nt], x[0], y[0], x[1], y[1], q.x, q.y);
+          mma_f16(s[nt], x[2], y[2], x[3], y[3], q.z, q.w);
         }
       }
     }
@@ -202,7 +213,7 @@ template <int D>
 __global__ void __launch_bounds__(kWThreads) weights_f32_kernel(WeightsArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   float4 *qs = reinterpret_cast<float4 *>(smem);  // [G][D / 4]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int g = lane >> 2, c = lane & 3;
   const int group = blockIdx.y, b = group / a.n_kv_heads, gk = group % a.n_kv_heads;
   const int G = a.n_q_heads / a.n_kv_heads;
@@ -210,15 +221,15 @@ __global__ void __launch_bounds__(kWThreads) weights_f32_kernel(WeightsArgs a) {
   grid_dependency_wait();
   const int n = n_tokens(a, b);
   const int tiles = (n + 7) / 8;
-  if (static_cast<int>(blockIdx.x) * kWWarps >= tiles) return;
+  if (static_cast<int>(blockIdx.x) * warps >= tiles) return;
   const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + head0 * D);
   float *lse = reinterpret_cast<float *>(qs + G * (D / 4));
-  for (int i = threadIdx.x; i < G * (D / 4); i += kWThreads) qs[i] = q[i];
-  for (int i = threadIdx.x; i < G; i += kWThreads) lse[i] = a.lse[head0 + i];
+  for (int i = threadIdx.x; i < G * (D / 4); i += blockDim.x) qs[i] = q[i];
+  for (int i = threadIdx.x; i < G; i += blockDim.x) lse[i] = a.lse[head0 + i];
   __syncthreads();
   const float *K = static_cast<const float *>(a.keys) + static_cast<size_t>(group) * a.max_ctx * D;
   float *out = a.weights + static_cast<size_t>(group) * a.max_ctx;
-  for (int tile = blockIdx.x * kWWarps + warp; tile < tiles; tile += gridDim.x * kWWarps) {
+  for (int tile = blockIdx.x * warps + warp; tile < tiles; tile += gridDim.x * warps) {
     const int t = token_at(a, group, tile * 8 + g, n);
     const float4 *row = reinterpret_cast<const float4 *>(K + static_cast<size_t>(max(t, 0)) * D);
     float4 k[D / 16];
@@ -244,12 +255,21 @@ __global__ void __launch_bounds__(kWThreads) weights_f32_kernel(WeightsArgs a) {
   }
 }
 
-// CTAs of a group: enough to fill the GPU several times over, no more than it has tiles.
-int split_of(const WeightsArgs &a, int tokens_per_cta, int ctas_per_sm) {
+// Threads of a CTA and CTAs of a group: as many as run at once (per_sm of 256
+// threads), no more than there are tiles; half-size CTAs where whole ones would
+// leave SMs without a tile.
+struct Split {
+  int threads, ctas;
+};
+Split split_of(const WeightsArgs &a, int tokens_per_warp, int per_sm) {
   const long long n = a.token_idx ? a.k_t : a.max_ctx;
   const long long groups = static_cast<long long>(a.batch) * a.n_kv_heads;
-  const long long fill = (static_cast<long long>(a.num_sms) * ctas_per_sm + groups - 1) / groups;
-  return static_cast<int>(std::max<long long>(1, std::min((n + tokens_per_cta - 1) / tokens_per_cta, fill)));
+  const long long sms = a.num_sms > 0 ? a.num_sms : 148;
+  const long long tiles = (n + tokens_per_warp - 1) / tokens_per_warp;
+  int warps = kWThreads / 32;
+  while (warps > 2 && groups * ((tiles + warps - 1) / warps) < sms) warps /= 2;
+  const long long fill = std::max<long long>(1, sms * per_sm / groups);
+  return {warps * 32, static_cast<int>(std::max<long long>(1, std::min((tiles + warps - 1) / warps, fill)))};
 }
 
 template <int D, int NT, int KIND>
@@ -266,9 +286,9 @@ cudaError_t run_mma(const WeightsArgs &a, cudaStream_t st) {
       if (dev >= 0 && dev < 64) configured[dev] = true;
     }
   }
-  const dim3 grid(split_of(a, 16 * kWWarps, L::kBytes > 100 * 1024 ? 1 : L::kBytes > 60 * 1024 ? 2 : 6),
-                  a.batch * a.n_kv_heads);
-  return launch_pdl(kern, grid, dim3(kWThreads), L::kBytes, st, a);
+  // resident CTAs an SM: five by registers, fewer where the latent's queries fill shared memory
+  const Split sp = split_of(a, 16, L::kBytes > 110 * 1024 ? 1 : L::kBytes > 70 * 1024 ? 3 : L::kBytes > 40 * 1024 ? 4 : 5);
+  return launch_pdl(kern, dim3(sp.ctas, a.batch * a.n_kv_heads), dim3(sp.threads), L::kBytes, st, a);
 }
 
 template <int D, int KIND>
@@ -286,8 +306,8 @@ template <int D>
 cudaError_t run_f32(const WeightsArgs &a, cudaStream_t st) {
   const int G = a.n_q_heads / a.n_kv_heads;
   const size_t smem = static_cast<size_t>(G) * (D + 1) * 4;  // at most 33 KB (64 heads of 128 channels)
-  return launch_pdl(weights_f32_kernel<D>, dim3(split_of(a, 8 * kWWarps, 6), a.batch * a.n_kv_heads), dim3(kWThreads),
-                    smem, st, a);
+  const Split sp = split_of(a, 8, 4);
+  return launch_pdl(weights_f32_kernel<D>, dim3(sp.ctas, a.batch * a.n_kv_heads), dim3(sp.threads), smem, st, a);
 }
 
 }  // namespace
