@@ -351,8 +351,9 @@ TLS_API tls_status tls_prefetch_diff(const tls_shape *s, int32_t n_slots, const 
 /* Bytes of the 4-bit cache; 0 for an invalid shape (see tls_last_error). */
 TLS_API size_t tls_kv4_cache_bytes(const tls_shape *s);
 
-/* Bytes of device workspace for tls_kv4_attn_decode (partials that only calls
- * with few groups use; at least 256); 0 for an invalid shape. */
+/* Bytes of device workspace for tls_kv4_attn_decode on the current device (the
+ * partials of calls that are cut into parts: few groups, or long lists); it
+ * depends on the heads per group and d alone.  0 for an invalid shape. */
 TLS_API size_t tls_kv4_workspace_size(const tls_shape *s);
 
 /* Quantises the rows of tokens [old_lens[b], new_lens[b]) of every sequence

@@ -667,10 +667,11 @@ static tls::Kv4AttnArgs kv4_attn_args(const tls_shape *s) {
   return a;
 }
 
-size_t tls_kv4_workspace_size(const tls_shape *s) {
-  if (check_kv4(s) != TLS_OK) return 0;
-  return std::max<size_t>(256, up256(tls::kv4_attn_part_floats(kv4_attn_args(s)) * sizeof(float)));
+static size_t kv4_workspace(const tls_shape *s) {
+  return up256(tls::kv4_attn_part_floats(s->n_q_heads / s->n_kv_heads, s->d_qk, device_sms()) * sizeof(float));
 }
+
+size_t tls_kv4_workspace_size(const tls_shape *s) { return check_kv4(s) == TLS_OK ? kv4_workspace(s) : 0; }
 
 tls_status tls_kv4_append(const tls_shape *s, const void *K, const void *V, const int32_t *old_lens,
                           const int32_t *new_lens, int32_t row_stride, const int32_t *label_idx, void *cache,
@@ -737,7 +738,7 @@ tls_status tls_kv4_attn_decode(const tls_shape *s, const void *q, const void *ca
   }
   CHECK_PTR(out, 16);
   if (lse_out) CHECK_PTR(lse_out, 4);
-  const size_t need = tls_kv4_workspace_size(s);
+  const size_t need = kv4_workspace(s);
   if (!ws || ws_bytes < need || !aligned(ws, 256))
     return fail(TLS_ERR_WORKSPACE, "workspace too small or not 256-byte aligned (need %zu bytes)", need);
   tls::Kv4AttnArgs a = kv4_attn_args(s);

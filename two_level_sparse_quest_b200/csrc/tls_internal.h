@@ -207,7 +207,7 @@ struct Kv4AttnArgs {
   int num_sms;
   int head_chunk, n_head_chunks, cluster, n_split;  // Kv4Plan
 };
-size_t kv4_attn_part_floats(const Kv4AttnArgs &a);  // workspace floats for either kind of call
+size_t kv4_attn_part_floats(int heads_per_group, int d, int num_sms);  // workspace floats of any call
 cudaError_t launch_kv4_attention(Kv4AttnArgs a, cudaStream_t st);
 
 // Softmax weights of a decode step added to one number per token (tls_weights.cu).

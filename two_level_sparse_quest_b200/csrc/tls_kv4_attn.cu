@@ -50,7 +50,7 @@ constexpr int kTile = 32;   // tokens per ring stage
 constexpr int kWarps = 8;   // per CTA
 constexpr int kRing = 3;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxSplit = 64;
+constexpr int kMaxSplit = 148;
 constexpr float kPShift = 14.f;     // P is scaled by 2^14
 constexpr float kNoMax = -3e38f;    // a warp's m before its first token: finite, so that a masked score stays -inf
 
@@ -623,6 +623,9 @@ __global__ void __launch_bounds__(kMergeGroups * D) kv4_merge_kernel(Kv4AttnArgs
   if (a.lse && ch == 0) a.lse[head] = ls == 0.f ? -INFINITY : (M + (log2f(ls) - kPShift)) * 0.69314718055994531f;
 }
 
+// Partials that a call may leave in the workspace, over all units.
+int max_parts(int sms) { return 4 * sms; }
+
 // How a call is cut: heads per unit, and either CTAs per cluster or parts per
 // unit (joined by a second launch), whichever this estimate in tenths of a
 // microsecond (fitted at d 128, 4 heads) finds cheaper.  A warp takes 1.9 us
@@ -635,18 +638,20 @@ void kv4_plan(Kv4AttnArgs &a, int n_max) {
   const int G = a.n_q_heads / a.n_kv_heads;
   a.head_chunk = std::min(G, 16);
   a.n_head_chunks = G / a.head_chunk;
-  const long long units = static_cast<long long>(a.batch) * a.n_kv_heads * a.n_head_chunks;
-  const long long sms = a.num_sms > 0 ? a.num_sms : 148;
-  const long long resident = a.head_chunk > 8 ? sms : 2 * sms;  // 16 heads: one CTA an SM (registers)
-  const long long tiles = std::max<long long>(1, (n_max + kTile - 1) / kTile);  // of one unit
+  const int units = a.batch * a.n_kv_heads * a.n_head_chunks;
+  const int sms = a.num_sms > 0 ? a.num_sms : 148;
+  const int resident = a.head_chunk > 8 ? sms : 2 * sms;              // 16 heads: one CTA an SM (registers)
+  const int tiles = std::max(1, (n_max + kTile - 1) / kTile);         // of one unit
+  const int most = (tiles + kWarps - 1) / kWarps;                     // CTAs of a unit that still have a tile for every warp
+  // clusters of 4 and 8 do not fill every GPC: 7/8 and 13/16 of the places (at one CTA an SM 132 and 120 of 148 run at once)
+  auto places = [&](int cluster) { return cluster == 8 ? resident * 13 / 16 : cluster == 4 ? resident * 7 / 8 : resident; };
   a.cluster = a.n_split = 1;
   long long best = -1;
   auto consider = [&](int cluster, int n_split) {
-    const long long per_unit = static_cast<long long>(cluster) * n_split, ctas = units * per_unit;
-    const long long rounds = (tiles + per_unit * kWarps - 1) / (per_unit * kWarps);
-    // clusters of 4 and 8 do not fill every GPC: 7/8 and 13/16 of the places (at one CTA an SM 132 and 120 of 148 run at once)
-    const long long places = cluster == 8 ? resident * 13 / 16 : cluster == 4 ? resident * 7 / 8 : resident;
-    const long long waves = (ctas + places - 1) / places;
+    const int per_unit = cluster * n_split;
+    const long long ctas = static_cast<long long>(units) * per_unit;
+    const int rounds = (tiles + per_unit * kWarps - 1) / (per_unit * kWarps);
+    const long long waves = (ctas + places(cluster) - 1) / places(cluster);
     const long long cost = waves * (35 + rounds * (ctas <= sms ? 11 : 19)) + (cluster > 1 ? 10 : 0) + (n_split > 1 ? 30 : 0);
     if (best < 0 || cost < best) {
       best = cost;
@@ -654,10 +659,13 @@ void kv4_plan(Kv4AttnArgs &a, int n_max) {
       a.n_split = n_split;
     }
   };
-  const long long most = (tiles + kWarps - 1) / kWarps;  // CTAs of a unit that still have a tile for every warp
   for (int c = 1; c <= kMaxCluster && (c == 1 || c <= most); c *= 2) consider(c, 1);
-  for (int c : {1, kMaxCluster})
-    for (int p = 2; p <= kMaxSplit && c * p <= most; ++p) consider(c, p);
+  for (int c : {1, kMaxCluster})  // as many parts as fill one to four waves
+    for (int w = 1; w <= 4; ++w) {
+      const int p = std::min({static_cast<int>(static_cast<long long>(w) * places(c) / (static_cast<long long>(units) * c)),
+                              most / c, kMaxSplit, max_parts(sms) / units});
+      if (p >= 2) consider(c, p);
+    }
 }
 
 template <int D, int NT, bool LIST, bool PAGED, bool F32OUT>
@@ -688,16 +696,8 @@ cudaError_t dispatch(const Kv4AttnArgs &a, cudaStream_t st) {
 
 }  // namespace
 
-size_t kv4_attn_part_floats(const Kv4AttnArgs &in) {
-  size_t most = 0;
-  for (int n : {in.k_t, in.max_ctx}) {
-    Kv4AttnArgs a = in;
-    kv4_plan(a, n);
-    if (a.n_split == 1) continue;
-    const size_t units = static_cast<size_t>(a.batch) * a.n_kv_heads * a.n_head_chunks;
-    most = std::max(most, units * a.n_split * a.head_chunk * (2 + a.d));
-  }
-  return most;
+size_t kv4_attn_part_floats(int heads_per_group, int d, int num_sms) {
+  return static_cast<size_t>(max_parts(num_sms > 0 ? num_sms : 148)) * std::min(heads_per_group, 16) * (2 + d);
 }
 
 cudaError_t launch_kv4_attention(Kv4AttnArgs a, cudaStream_t st) {

@@ -144,14 +144,21 @@ def _dptr(x):
 def _dptrs(*xs):
     """_dptr of several arguments, whose tensors must lie on the current device
     (the one that the call launches on)."""
-    dev, out = None, []
+    cur, out = -2, []
     for x in xs:
-        out.append(_dptr(x))
         if isinstance(x, torch.Tensor):
-            if dev is None:
-                dev = torch.cuda.current_device()
-            if x.get_device() != dev:
-                raise ValueError(f"tensor on cuda:{x.get_device()}, but the current device is cuda:{dev}")
+            dev = x.get_device()  # -1: host memory
+            if dev != cur:
+                if dev < 0:
+                    raise ValueError("expected a CUDA tensor (the kernels address device memory)")
+                cur = torch.cuda.current_device()
+                if dev != cur:
+                    raise ValueError(f"tensor on cuda:{dev}, but the current device is cuda:{cur}")
+            if not x.is_contiguous():
+                raise ValueError("tensor must be contiguous")
+            out.append(x.data_ptr())
+        else:
+            out.append(_ptr(x))
     return out
 
 
