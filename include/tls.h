@@ -398,6 +398,17 @@ TLS_API tls_status tls_kv4_attn_decode(const tls_shape *s, const void *q, const 
                                        const int32_t *slot_of_block, int32_t n_slots, void *out, float *lse_out,
                                        void *ws, size_t ws_bytes, void *stream);
 
+/* tls_prefetch_diff for blocks of the 4-bit cache: 3.6 times fewer bytes over
+ * PCIe than bf16.  Arguments and slot tables as there (tls_offload_reset), with
+ *   host_kv  pinned host [B][H_kv][ceil(max_ctx/bs)][bs] records
+ *   cache    device [B][H_kv][n_slots][bs] records (tls_kv4_attn_decode with
+ *            slot_of_block)
+ * A block's bytes must be a multiple of 16: at d 64 an even block_size. */
+TLS_API tls_status tls_kv4_prefetch_diff(const tls_shape *s, int32_t n_slots, const void *host_kv, void *cache,
+                                         int32_t *slot_of_block, int32_t *block_of_slot,
+                                         const int32_t *prev_block_idx, const int32_t *next_block_idx,
+                                         int32_t *n_new_out, int32_t *jobs_ws, void *stream);
+
 /* ---- eviction by accumulated attention weight ---------------------------------
  * (no counterpart in the paper: an addition of this library.)  A decode loop
  * adds up the attention weight of every cached token; when the cache has to

@@ -94,6 +94,24 @@ def test_kv4_attention_refusals(T):
     assert attn(T, good(T, batch=0), q=None, cache=None, out=None, ws=None) == T.TLS_OK
 
 
+def test_kv4_prefetch_refusals(T):
+    call = lambda s, n=384, host=256, cache=256, prev=None, nxt=256: T._lib.tls_kv4_prefetch_diff(
+        by(s), n, host, cache, 256, 256, prev, nxt, 256, 256, None)
+    s = good(T)
+    for kw, word in ((dict(n=0), "n_slots"), (dict(n=5000), "n_slots"), (dict(host=None), "host_kv"),
+                     (dict(cache=264), "cache"), (dict(prev=258), "prev_block_idx"), (dict(nxt=None), "next_block_idx")):
+        assert call(s, **kw) == T.TLS_ERR_INVALID_ARG and word in T.tls_last_error(), kw
+    assert call(good(T, kv_dtype=T.TLS_F32)) == T.TLS_ERR_UNSUPPORTED
+    assert call(good(T, d_qk=64, d_v=64, block_size=7)) == T.TLS_ERR_UNSUPPORTED and "even" in T.tls_last_error()
+    assert call(good(T, batch=0), host=None, cache=None, nxt=None) == T.TLS_OK
+
+
+def test_lists_beyond_int_are_refused(T):
+    s = good(T, k_t=2 ** 30 + 1)
+    assert attn(T, s) == T.TLS_ERR_UNSUPPORTED and "k_t" in T.tls_last_error()
+    assert T._lib.tls_accum_weights(by(s), 256, 256, 256, None, 256, 256, None) == T.TLS_ERR_UNSUPPORTED
+
+
 def test_accum_weights_refusals(T):
     call = lambda s, q=256, K=256, tok=256, lens=256, lse=256, w=256: T._lib.tls_accum_weights(by(s), q, K, tok, lens, lse, w, None)
     s = good(T)

@@ -261,6 +261,28 @@ def test_compact_caller_list_shorter_than_the_budget(T):
     run_compact(T, 1, 2, 100, [90], 50, [[np.array([3, 50, 89]), np.array([], np.int64)]], [16])
 
 
+def test_eviction_of_a_very_long_cache(T):
+    """Ids and byte offsets far out: 17 million tokens, rows beyond 4 GiB."""
+    ctx, budget = 17_000_000, 1000
+    s = make(T, 1, 1, 1, 64, ctx, bs=2048)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    w = torch.rand((1, 1, ctx), generator=g, device="cuda")
+    far = torch.randperm(ctx, generator=g, device="cuda")[:budget - 20].sort().values
+    w[0, 0, far] += 2 + torch.rand(budget - 20, generator=g, device="cuda")
+    rows = torch.randint(0, 256, (1, 1, ctx, 256), generator=g, device="cuda", dtype=torch.uint8)  # 4.4 GB
+    keep, new = torch.zeros((1, 1, budget), dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    T.tls_evict_select(s, budget, 4, 16, w, i32([ctx]), keep, new)
+    torch.cuda.synchronize()
+    got = keep[0, 0].long()
+    must = torch.cat((torch.arange(4, device="cuda"), far, torch.arange(ctx - 16, ctx, device="cuda"))).unique()
+    assert new.item() == budget and (got[1:] > got[:-1]).all() and torch.isin(must, got).all()
+    want, ww, tail = rows[0, 0, got].clone(), w[0, 0, got].clone(), rows[0, 0, -5000:].clone()
+    T.tls_evict_compact(s, budget, keep, i32([ctx]), [rows], w)
+    torch.cuda.synchronize()
+    assert torch.equal(rows[0, 0, :budget], want) and torch.equal(rows[0, 0, -5000:], tail)
+    assert torch.equal(w[0, 0, :budget], ww) and not w[0, 0, budget:].any()
+
+
 # --------------------------------------------------------------------------------------- used together
 def test_decode_loop_over_a_4bit_cache_with_eviction(T):
     """A prompt into the 4-bit cache, decode steps that append a token, select, attend and add up weights, and an

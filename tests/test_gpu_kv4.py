@@ -365,3 +365,101 @@ def test_attention_on_a_stream_and_in_a_graph(T):
             g.replay()
         torch.cuda.synchronize()
         assert torch.equal(outs[0], want[i]) and torch.equal(outs[1], want[i])
+
+
+@pytest.mark.parametrize("kscale,vscale", [(2e-4, 1e-4), (1.0, 1e-4), (3e-5, 20000.0), (100.0, 1.0)])
+def test_attention_of_small_and_large_rows(T, kscale, vscale):
+    """Scales down to the smallest (values that are subnormal in fp16) and up to the clamp."""
+    rng = np.random.default_rng(13)
+    d, ctx, H, G = 128, 300, 2, 4
+    rec = R.records(rng.standard_normal((1, H, ctx, d)) * kscale, rng.standard_normal((1, H, ctx, d)) * vscale)
+    s = shape(T, 1, H, G, d, ctx)
+    s.softmax_scale = 0.3 / kscale
+    q = bf16_rows(rng, (1, H * G, d), 0.2, False)
+    out, lse = torch.zeros((1, H * G, d), device="cuda"), torch.zeros((1, H * G), device="cuda")
+    T.tls_kv4_attn_decode(s, q.cuda(), torch.from_numpy(rec).cuda(), out, lse, seq_lens=i32([ctx]),
+                          ws=torch.zeros(T.tls_kv4_workspace_size(s), dtype=torch.uint8, device="cuda"))
+    for h in range(H):
+        hs = slice(h * G, (h + 1) * G)
+        wo, wl, tol, ltol = R.attention(f64(q[0, hs]), *R.split(rec[0, h], d), range(ctx), float(s.softmax_scale))
+        assert (np.abs(f64(out[0, hs]) - wo) <= tol).all() and (np.abs(f64(lse[0, hs]) - wl) <= ltol).all()
+
+
+def test_rows_beyond_4_gib(T):
+    """Records whose byte offsets pass 32 bits: stored, read back, attended and weighed."""
+    d, ctx = 128, 31_000_000
+    s = shape(T, 1, 1, 4, d, ctx, bs=2048, kt=40)
+    cache = torch.zeros((1, 1, ctx, 144), dtype=torch.uint8, device="cuda")  # 4.5 GB
+    rng = np.random.default_rng(21)
+    n, first = 50, ctx - 50
+    K, V = bf16_rows(rng, (1, 1, n, d)), bf16_rows(rng, (1, 1, n, d), 1.0, False)
+    T.tls_kv4_append(s, K.cuda(), V.cuda(), i32([first]), i32([ctx]), n, cache)
+    out = torch.zeros((1, 1, n, d), dtype=BF16, device="cuda")
+    T.tls_kv4_read(s, cache, i32([first]), i32([ctx]), n, out)
+    code, b = R.quantise(f64(K))
+    np.testing.assert_array_equal(f64(out), R.value(code, b))
+    assert (cache[0, 0, :first].view(-1, 144)[-1000:] == 0).all() and (cache[0, 0, 0] == 0).all()
+    rec = R.records(f64(K), f64(V))[0, 0]
+    tok = np.sort(rng.permutation(n)[:40])
+    q = bf16_rows(rng, (1, 4, d), 1.0, False)
+    o, lse = torch.zeros((1, 4, d), device="cuda"), torch.zeros((1, 4), device="cuda")
+    T.tls_kv4_attn_decode(s, q.cuda(), cache, o, lse, token_idx=i32([[(tok + first).tolist()]]),
+                          ws=torch.zeros(T.tls_kv4_workspace_size(s), dtype=torch.uint8, device="cuda"))
+    Kv, Vv = R.split(rec, d)
+    wo, wl, tol, _ = R.attention(f64(q[0]), Kv, Vv, tok, 1 / np.sqrt(d))
+    assert (np.abs(f64(o[0]) - wo) <= tol).all()
+    w = torch.zeros((1, 1, ctx), device="cuda")
+    T.tls_kv4_accum_weights(s, q.cuda(), cache, lse, w, token_idx=i32([[(tok + first).tolist()]]))
+    add, wtol = R.weights(f64(q[0]), Kv, f64(lse[0]), tok, 1 / np.sqrt(d), n)
+    assert (np.abs(f64(w[0, 0, first:]) - add) <= wtol + 4 * R.U32 * add).all() and (w[0, 0, :first] == 0).all()
+
+
+@pytest.mark.parametrize("d,bs", [(128, 32), (128, 7), (64, 16)])
+def test_prefetched_blocks_are_attended(T, d, bs):
+    """A stream of selections over 4-bit blocks in pinned host memory: each step copies the blocks that entered,
+    and the attention over the slot cache gives the bits of the attention over the whole cache."""
+    rng = np.random.default_rng(bs)
+    B, H, G, ctx, kb = 2, 2, 4, 40 * bs - 3, 6
+    nb, kt, rb = -(-ctx // bs), 3 * bs, 9 * d // 8
+    n_slots = 2 * kb
+    s = T.make_shape(batch=B, n_q_heads=H * G, n_kv_heads=H, d_qk=d, d_v=d, block_size=bs, n_label=16, k_b=kb, k_t=kt,
+                     max_ctx=ctx, kv_dtype=T.TLS_BF16)
+    rec = R.records(rng.standard_normal((B, H, ctx, d)), rng.standard_normal((B, H, ctx, d)))
+    host = torch.zeros((B, H, nb * bs, rb), dtype=torch.uint8).pin_memory()
+    host[:, :, :ctx] = torch.from_numpy(rec)
+    whole = torch.from_numpy(rec).cuda()
+    dev = dict(dtype=torch.int32, device="cuda")
+    cache = torch.full((B, H, n_slots, bs, rb), 0xFF, dtype=torch.uint8, device="cuda")
+    sob, bos = torch.empty((B, H, nb), **dev), torch.empty((B, H, n_slots), **dev)
+    n_new, jobs = torch.empty((B, H), **dev), torch.empty((B, H, kb, 2), **dev)
+    ws = torch.zeros(T.tls_kv4_workspace_size(s), dtype=torch.uint8, device="cuda")
+    T.tls_offload_reset(s, n_slots, sob, bos)
+    prev, held, resident = None, [[set() for _ in range(H)] for _ in range(B)], [[set() for _ in range(H)] for _ in range(B)]
+    for step in range(6):
+        sel = [[rng.permutation(sorted(held[b][h]))[:3].astype(int).tolist() for h in range(H)] for b in range(B)]
+        for b in range(B):
+            for h in range(H):
+                rest = [x for x in rng.permutation(nb).tolist() if x not in sel[b][h]]
+                sel[b][h] = sorted(sel[b][h] + rest[:kb - len(sel[b][h])])
+        nxt = i32(sel)
+        T.tls_kv4_prefetch_diff(s, n_slots, host, cache, sob, bos, prev, nxt, n_new, jobs)
+        tok = np.full((B, H, kt), -1)
+        for b in range(B):
+            for h in range(H):
+                cand = np.concatenate([np.arange(x * bs, min((x + 1) * bs, ctx)) for x in sel[b][h]])
+                pick = np.sort(rng.permutation(cand)[:kt])
+                tok[b, h, :len(pick)] = pick
+        q = bf16_rows(rng, (B, H * G, d), 1.0, False).cuda()
+        outs = [torch.zeros((B, H * G, d), device="cuda") for _ in range(2)]
+        T.tls_kv4_attn_decode(s, q, cache, outs[0], token_idx=i32(tok.tolist()), slot_of_block=sob, n_slots=n_slots, ws=ws)
+        T.tls_kv4_attn_decode(s, q, whole, outs[1], token_idx=i32(tok.tolist()), ws=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], outs[1]) and outs[0].isfinite().all()
+        for b in range(B):
+            for h in range(H):
+                # a block stays resident while the previous or the next selection holds it
+                assert n_new[b, h].item() == len(set(sel[b][h]) - resident[b][h])
+                resident[b][h] = held[b][h] | set(sel[b][h])
+                held[b][h] = set(sel[b][h])
+        prev = nxt
+    assert T.tls_device_error(clear=True) == 0

@@ -534,11 +534,11 @@ tls_status tls_offload_reset(const tls_shape *s, int32_t n_slots, int32_t *slot_
   return cuda_status(tls::launch_offload_reset(a, static_cast<cudaStream_t>(stream)), "offload_reset launch");
 }
 
-tls_status tls_prefetch_diff(const tls_shape *s, int32_t n_slots, const void *host_kv, void *cache,
-                             int32_t *slot_of_block, int32_t *block_of_slot, const int32_t *prev_block_idx,
-                             const int32_t *next_block_idx, int32_t *n_new_out, int32_t *jobs_ws, void *stream) {
-  tls_status st = offload_check(s, n_slots);
-  if (st != TLS_OK) return st;
+// block_bytes: of one block in host_kv and in a slot (a multiple of 16).
+static tls_status prefetch_diff(const tls_shape *s, int32_t n_slots, long long block_bytes, const void *host_kv,
+                                void *cache, int32_t *slot_of_block, int32_t *block_of_slot,
+                                const int32_t *prev_block_idx, const int32_t *next_block_idx, int32_t *n_new_out,
+                                int32_t *jobs_ws, void *stream) {
   if (s->batch == 0) return TLS_OK;
   CHECK_PTR(host_kv, 16);
   CHECK_PTR(cache, 16);
@@ -565,13 +565,20 @@ tls_status tls_prefetch_diff(const tls_shape *s, int32_t n_slots, const void *ho
   a.jobs = jobs_ws;
   a.batch = s->batch;
   a.n_kv_heads = s->n_kv_heads;
-  a.d = s->d_qk;
-  a.block_size = s->block_size;
   a.n_blocks_max = n_blocks_max(s);
   a.k_b = s->k_b;
   a.n_slots = n_slots;
-  a.dtype = s->kv_dtype;
+  a.block_bytes = static_cast<int>(block_bytes);
   return cuda_status(tls::launch_prefetch_diff(a, static_cast<cudaStream_t>(stream)), "prefetch_diff launch");
+}
+
+tls_status tls_prefetch_diff(const tls_shape *s, int32_t n_slots, const void *host_kv, void *cache,
+                             int32_t *slot_of_block, int32_t *block_of_slot, const int32_t *prev_block_idx,
+                             const int32_t *next_block_idx, int32_t *n_new_out, int32_t *jobs_ws, void *stream) {
+  tls_status st = offload_check(s, n_slots);
+  if (st != TLS_OK) return st;
+  return prefetch_diff(s, n_slots, 2LL * s->block_size * s->d_qk * (s->kv_dtype == TLS_BF16 ? 2 : 4), host_kv, cache,
+                       slot_of_block, block_of_slot, prev_block_idx, next_block_idx, n_new_out, jobs_ws, stream);
 }
 
 tls_status tls_decode_step(const tls_shape *s, const void *q, const void *meta, const void *slab,
@@ -623,6 +630,17 @@ static tls_status check_kv4(const tls_shape *s) {
   if (st != TLS_OK) return st;
   if (s->v_is_k_prefix) return fail(TLS_ERR_UNSUPPORTED, "the 4-bit cache holds GQA K/V rows only");
   if (s->kv_dtype != TLS_BF16) return fail(TLS_ERR_UNSUPPORTED, "the 4-bit cache takes bf16 rows and queries");
+  return TLS_OK;
+}
+
+// The tokens of a call: a list, or every token below seq_lens.
+static tls_status check_tokens(const tls_shape *s, const int32_t *token_idx, const int32_t *seq_lens) {
+  if (token_idx) {
+    CHECK_PTR(token_idx, 4);
+    if (s->k_t > (1 << 30)) return fail(TLS_ERR_UNSUPPORTED, "k_t %d > 2^30", s->k_t);  // kernels round it up in int
+  } else {
+    CHECK_PTR(seq_lens, 4);
+  }
   return TLS_OK;
 }
 
@@ -727,8 +745,8 @@ tls_status tls_kv4_attn_decode(const tls_shape *s, const void *q, const void *ca
   if (s->batch == 0) return TLS_OK;
   CHECK_PTR(q, 16);
   CHECK_PTR(cache, 16);
-  if (token_idx) CHECK_PTR(token_idx, 4);
-  else CHECK_PTR(seq_lens, 4);
+  st = check_tokens(s, token_idx, seq_lens);
+  if (st != TLS_OK) return st;
   if (slot_of_block) {
     if (!token_idx) return fail(TLS_ERR_UNSUPPORTED, "a slot cache is attended through token_idx");
     CHECK_PTR(slot_of_block, 4);
@@ -755,6 +773,20 @@ tls_status tls_kv4_attn_decode(const tls_shape *s, const void *q, const void *ca
   return cuda_status(tls::launch_kv4_attention(a, static_cast<cudaStream_t>(stream)), "kv4_attention launch");
 }
 
+tls_status tls_kv4_prefetch_diff(const tls_shape *s, int32_t n_slots, const void *host_kv, void *cache,
+                                 int32_t *slot_of_block, int32_t *block_of_slot, const int32_t *prev_block_idx,
+                                 const int32_t *next_block_idx, int32_t *n_new_out, int32_t *jobs_ws, void *stream) {
+  tls_status st = check_kv4(s);
+  if (st != TLS_OK) return st;
+  st = offload_check(s, n_slots);
+  if (st != TLS_OK) return st;
+  const long long block_bytes = static_cast<long long>(s->block_size) * (9 * s->d_qk / 8);
+  if (block_bytes % 16)  // the copy moves 16 bytes at a time
+    return fail(TLS_ERR_UNSUPPORTED, "4-bit blocks of %lld bytes: d 64 needs an even block_size", block_bytes);
+  return prefetch_diff(s, n_slots, block_bytes, host_kv, cache, slot_of_block, block_of_slot, prev_block_idx,
+                       next_block_idx, n_new_out, jobs_ws, stream);
+}
+
 // ---- accumulated attention weight, eviction
 static tls_status accum_weights(const tls_shape *s, const void *q, const void *keys, int kind,
                                 const int32_t *token_idx, const int32_t *seq_lens, const float *lse, float *weights,
@@ -762,8 +794,8 @@ static tls_status accum_weights(const tls_shape *s, const void *q, const void *k
   if (s->batch == 0) return TLS_OK;
   CHECK_PTR(q, 16);
   CHECK_PTR(keys, 16);
-  if (token_idx) CHECK_PTR(token_idx, 4);
-  else CHECK_PTR(seq_lens, 4);
+  const tls_status st = check_tokens(s, token_idx, seq_lens);
+  if (st != TLS_OK) return st;
   CHECK_PTR(lse, 4);
   CHECK_PTR(weights, 4);
   tls::WeightsArgs a{};

@@ -166,9 +166,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
   // The ring.  Neighbouring tokens at d 128 (a record is a multiple of 16
   // bytes) come with one bulk copy a stage, counted by the stage's mbarrier;
   // tokens past the end get zero scales, so that stale bytes stay finite.
-  // Listed tokens come with cp.async, nine chunks of d / 8 bytes a record,
-  // zero-filled: eight lanes bring a record's first eight chunks, then every
-  // lane its own record's ninth.  (One bulk copy per listed record was slower:
+  // Listed tokens come with cp.async, nine chunks of d / 8 bytes a record; where
+  // some are missing, eight lanes bring a record's first eight chunks and every
+  // lane its own record's ninth, zero-filled.  (One bulk copy per listed record was slower:
   // 24.0 us against 20.4 for 8 x 96k, 4096 tokens.)
   uint32_t valid[kRing];  // valid tokens of the stages in flight, oldest first
 #pragma unroll
@@ -197,15 +197,15 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
       } else {
         constexpr int CB = R::kChunk;
         const uint32_t dst = ring_s + stage_issue * L::kStage;
-        const unsigned char *src = base + (lane & 7) * CB;
         if (mask == 0xffffffffu) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const long long u = __shfl_sync(0xffffffffu, row, 4 * i + (lane >> 3));
-            cp_async_chunk<CB>(dst + (4 * i + (lane >> 3)) * R::kBytes + (lane & 7) * CB, src + u * R::kBytes);
+          for (int i = 0; i < 9; ++i) {  // neighbouring lanes on neighbouring bytes
+            const int idx = i * 32 + lane, tk = (idx * 57) >> 9;  // idx / 9 for idx < 288
+            const long long u = __shfl_sync(0xffffffffu, row, tk);
+            cp_async_chunk<CB>(dst + idx * CB, base + (u - tk) * R::kBytes + idx * CB);
           }
-          cp_async_chunk<CB>(dst + lane * R::kBytes + 8 * CB, base + static_cast<long long>(row) * R::kBytes + 8 * CB);
         } else {
+          const unsigned char *src = base + (lane & 7) * CB;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const long long u = __shfl_sync(0xffffffffu, row, 4 * i + (lane >> 3));

@@ -5,7 +5,7 @@
 // 2.B "Transferencia Incremental").
 //
 // The full KV cache stays in pinned host memory, one block per contiguous
-// range ([2][bs][d]: K rows then V rows).  The GPU holds a slot cache with a
+// range ([2][bs][d]: K rows then V rows; or bs records of the 4-bit cache).  The GPU holds a slot cache with a
 // per-group slot table.  prefetch_diff_kernel (one CTA per group) evicts the
 // resident blocks that neither the previous nor the next selection holds,
 // assigns free slots (lowest first) to the blocks of the next selection that
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kDiffThreads) prefetch_diff_kernel(OffloadArgs
   if (threadIdx.x == 0) a.n_new[group] = n_new;
 }
 
-// One CTA per (job, group); a job is one block of 2 * bs * d elements.
+// One CTA per (job, group); a job is one block (2 * bs * d elements, or bs 4-bit records).
 __global__ void __launch_bounds__(256) copy_blocks_kernel(OffloadArgs a, int block_bytes) {
   grid_dependency_wait();
   const int group = blockIdx.y, q = blockIdx.x;
@@ -146,8 +146,7 @@ cudaError_t launch_prefetch_diff(const OffloadArgs &a, cudaStream_t st) {
   const int groups = a.batch * a.n_kv_heads;
   cudaError_t e = launch_pdl(prefetch_diff_kernel, dim3(groups), dim3(kDiffThreads), 0, st, a);
   if (e != cudaSuccess) return e;
-  const int block_bytes = 2 * a.block_size * a.d * (a.dtype == 1 ? 2 : 4);
-  return launch_pdl(copy_blocks_kernel, dim3(a.k_b, groups), dim3(256), 0, st, a, block_bytes);
+  return launch_pdl(copy_blocks_kernel, dim3(a.k_b, groups), dim3(256), 0, st, a, a.block_bytes);
 }
 
 }  // namespace tls

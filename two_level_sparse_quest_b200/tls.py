@@ -33,7 +33,7 @@ EXPORTED = ("tls_version", "tls_last_error", "tls_workspace_size", "tls_build_bl
             "tls_prefetch_diff", "tls_wait_event", "tls_block_score_topk_noalloc", "tls_device_error", "tls_select_step",
             "tls_append_tokens", "tls_slab_bytes", "tls_noalloc_read_scores", "tls_decode_step", "tls_select_step_ws",
             "tls_kv4_cache_bytes", "tls_kv4_workspace_size", "tls_kv4_append", "tls_kv4_read", "tls_kv4_attn_decode",
-            "tls_accum_weights", "tls_kv4_accum_weights", "tls_evict_select", "tls_evict_compact")
+            "tls_kv4_prefetch_diff", "tls_accum_weights", "tls_kv4_accum_weights", "tls_evict_select", "tls_evict_compact")
 
 
 class TlsShape(ctypes.Structure):
@@ -82,6 +82,7 @@ _sigs = {
     "tls_kv4_append": ([_S, _P, _P, _P, _P, _i32, _P, _P, _P, _P, _P], ctypes.c_int),
     "tls_kv4_read": ([_S, _P, _P, _P, _i32, _P, _P, _P], ctypes.c_int),
     "tls_kv4_attn_decode": ([_S, _P, _P, _P, _P, _P, _i32, _P, _P, _P, _sz, _P], ctypes.c_int),
+    "tls_kv4_prefetch_diff": ([_S, _i32, _P, _P, _P, _P, _P, _P, _P, _P, _P], ctypes.c_int),
     "tls_accum_weights": ([_S, _P, _P, _P, _P, _P, _P, _P], ctypes.c_int),
     "tls_kv4_accum_weights": ([_S, _P, _P, _P, _P, _P, _P, _P], ctypes.c_int),
     "tls_evict_select": ([_S, _i32, _i32, _i32, _P, _P, _P, _P, _P], ctypes.c_int),
@@ -332,6 +333,14 @@ def tls_kv4_attn_decode(shape, q, cache, out, lse_out=None, token_idx=None, seq_
     pq, pc, pt, pn, ps, po, pl = _dptrs(q, cache, token_idx, seq_lens, slot_of_block, out, lse_out)
     _check(_lib.tls_kv4_attn_decode(ctypes.byref(shape), pq, pc, pt, pn, ps, int(n_slots), po, pl, wp, wb,
                                     _stream(stream)), "tls_kv4_attn_decode")
+
+
+def tls_kv4_prefetch_diff(shape, n_slots, host_kv, cache, slot_of_block, block_of_slot, prev_block_idx, next_block_idx,
+                          n_new_out, jobs_ws, stream=None):
+    """tls_prefetch_diff for blocks of the 4-bit cache."""
+    ptrs = _dptrs(cache, slot_of_block, block_of_slot, prev_block_idx, next_block_idx, n_new_out, jobs_ws)
+    _check(_lib.tls_kv4_prefetch_diff(ctypes.byref(shape), int(n_slots), _hptr(host_kv), *ptrs, _stream(stream)),
+           "tls_kv4_prefetch_diff")
 
 
 def tls_accum_weights(shape, q, K, lse, weights, token_idx=None, seq_lens=None, stream=None):
