@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, 
   };
   const bool wide = (reinterpret_cast<size_t>(w) & 15) == 0;
   auto weights_at = [&](int i) -> float4 {
-    if (wide && i + 4 <= n) return __ldg(reinterpret_cast<const float4 *>(w + i));
+    if (wide && i + 4 <= n) return *reinterpret_cast<const float4 *>(w + i);
     return make_float4(i < n ? w[i] : 0.f, i + 1 < n ? w[i + 1] : 0.f, i + 2 < n ? w[i + 2] : 0.f, i + 3 < n ? w[i + 3] : 0.f);
   };
   auto keys_at = [&](int i) -> uint4 {
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, 
   if (CS > 1) cluster_arrive_release();  // waited for before the first add into another CTA's sums
 
   // the weights, once: keys into shared memory, counts of the first digit
-  constexpr int U = 2;  // reads of four weights in flight per thread
+  constexpr int U = 4;  // reads of four weights in flight per thread
   int zeros = 0;        // keys of weight zero seen by this thread
   auto count = [&](uint32_t key) {
     if (key == kZeroKey) ++zeros;

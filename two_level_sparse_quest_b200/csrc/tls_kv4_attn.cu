@@ -170,6 +170,14 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
   // some are missing, eight lanes bring a record's first eight chunks and every
   // lane its own record's ninth, zero-filled.  (One bulk copy per listed record was slower:
   // 24.0 us against 20.4 for 8 x 96k, 4096 tokens.)
+  // The queries' loads go out first (warps below NT, one block of 8 heads each).
+  uint4 qv[D / 32];
+  if (warp < NT) {
+    const uint4 *qp = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) +
+                                                      (static_cast<size_t>(b) * a.n_q_heads + head0 + warp * 8 + g) * D + c * (D / 4));
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) qv[i] = warp * 8 + g < HG ? qp[i] : make_uint4(0u, 0u, 0u, 0u);
+  }
   uint32_t valid[kRing];  // valid tokens of the stages in flight, oldest first
 #pragma unroll
   for (int s = 0; s < kRing; ++s) valid[s] = 0;
@@ -237,15 +245,12 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
     const int h = warp * 8 + g;
     uint32_t w[D / 8];
     uint32_t ex = 0;
-    const uint4 *qp = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) +
-                                                      (static_cast<size_t>(b) * a.n_q_heads + head0 + h) * D + c * (D / 4));
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-      const uint4 v = h < HG ? qp[i] : make_uint4(0u, 0u, 0u, 0u);
-      w[4 * i] = v.x;
-      w[4 * i + 1] = v.y;
-      w[4 * i + 2] = v.z;
-      w[4 * i + 3] = v.w;
+      w[4 * i] = qv[i].x;
+      w[4 * i + 1] = qv[i].y;
+      w[4 * i + 2] = qv[i].z;
+      w[4 * i + 3] = qv[i].w;
     }
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) ex = max(ex, bf16_exps(w[i]));

@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kWThreads) weights_f32_kernel(WeightsArgs a) {
     const float4 *row = reinterpret_cast<const float4 *>(K + static_cast<size_t>(max(t, 0)) * D);
     float4 k[D / 16];
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) k[i] = __ldg(row + 4 * i + c);
+    for (int i = 0; i < D / 16; ++i) k[i] = row[4 * i + c];
     float w = 0.f;
     for (int h = 0; h < G; ++h) {
       float s0 = 0.f, s1 = 0.f;
