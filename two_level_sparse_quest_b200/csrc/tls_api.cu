@@ -17,6 +17,7 @@
 #include <thread>
 
 #include "tls.h"
+#include "tls_cache.h"
 #include "tls_internal.h"
 
 namespace {
@@ -568,8 +569,8 @@ static tls_status prefetch_diff(const tls_shape *s, int32_t n_slots, long long b
   a.n_blocks_max = n_blocks_max(s);
   a.k_b = s->k_b;
   a.n_slots = n_slots;
-  a.block_bytes = static_cast<int>(block_bytes);
-  return cuda_status(tls::launch_prefetch_diff(a, static_cast<cudaStream_t>(stream)), "prefetch_diff launch");
+  return cuda_status(tls::launch_prefetch_diff_bytes(a, static_cast<int>(block_bytes), static_cast<cudaStream_t>(stream)),
+                     "prefetch_diff launch");
 }
 
 tls_status tls_prefetch_diff(const tls_shape *s, int32_t n_slots, const void *host_kv, void *cache,
@@ -577,6 +578,7 @@ tls_status tls_prefetch_diff(const tls_shape *s, int32_t n_slots, const void *ho
                              const int32_t *next_block_idx, int32_t *n_new_out, int32_t *jobs_ws, void *stream) {
   tls_status st = offload_check(s, n_slots);
   if (st != TLS_OK) return st;
+  // at most 16384 tokens a block (the shape checks): within int
   return prefetch_diff(s, n_slots, 2LL * s->block_size * s->d_qk * (s->kv_dtype == TLS_BF16 ? 2 : 4), host_kv, cache,
                        slot_of_block, block_of_slot, prev_block_idx, next_block_idx, n_new_out, jobs_ws, stream);
 }

@@ -24,8 +24,8 @@
 // Both are bound by HBM: 4 bytes a token, and each kept row once in and out.
 #include <algorithm>
 
+#include "tls_cache.h"
 #include "tls_device.cuh"
-#include "tls_internal.h"
 
 namespace tls {
 namespace {

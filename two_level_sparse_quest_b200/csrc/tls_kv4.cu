@@ -12,7 +12,7 @@
 // Both are one pass over the rows, bound by HBM.
 #include <algorithm>
 
-#include "tls_internal.h"
+#include "tls_cache.h"
 #include "tls_kv4.cuh"
 
 namespace tls {

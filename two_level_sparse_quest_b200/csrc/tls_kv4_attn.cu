@@ -39,7 +39,7 @@
 // (kv4_plan).
 #include <algorithm>
 
-#include "tls_internal.h"
+#include "tls_cache.h"
 #include "tls_kv4.cuh"
 #include "tls_mma.cuh"
 

@@ -23,7 +23,7 @@
 // holds a token twice adds it twice.
 #include <algorithm>
 
-#include "tls_internal.h"
+#include "tls_cache.h"
 #include "tls_kv4.cuh"
 #include "tls_mma.cuh"
 
