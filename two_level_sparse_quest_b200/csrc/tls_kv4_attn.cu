@@ -232,11 +232,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
     return mask;
   };
 
-#pragma unroll
-  for (int s = 0; s < kRing - 1; ++s) {
-    valid[s + 1] = issue();
-    if constexpr (!kBulk) cp_async_commit();
-  }
+  valid[1] = issue();
+  if constexpr (!kBulk) cp_async_commit();
 
   // Queries: B fragments of S^T = K q^T in shared memory, two MMA steps a
   // read.  Lane (g, c) holds head 8 nt + g's channels c D/4 .. + D/4 - 1, four
@@ -265,6 +262,12 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
     if (c == 0) s_scale[h] = a.scale_log2 * undo;
   }
   __syncthreads();
+  // the second stage once every warp has asked for its first: its bytes would only delay theirs
+#pragma unroll
+  for (int s = 1; s < kRing - 1; ++s) {
+    valid[s + 1] = issue();
+    if constexpr (!kBulk) cp_async_commit();
+  }
   float sl[NT][2];  // score scale of this lane's columns (heads 8 nt + 2c, + 1)
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
