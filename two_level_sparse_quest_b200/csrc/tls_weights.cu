@@ -61,7 +61,7 @@ struct WeightsSmem {
 };
 
 template <int D, int NT, int KIND>
-__global__ void __launch_bounds__(kWThreads) weights_mma_kernel(WeightsArgs a) {
+__global__ void __launch_bounds__(kWThreads, NT == 1 && D <= 128 ? 5 : 1) weights_mma_kernel(WeightsArgs a) {
   using L = WeightsSmem<D, NT, KIND>;
   constexpr int KS = L::KS;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -87,10 +87,14 @@ __global__ void __launch_bounds__(kWThreads) weights_mma_kernel(WeightsArgs a) {
 
   // B fragments: lane (g, c) of block nt: the 8 channels 32 i + 8 c of head 8 nt + g, steps 2 i and 2 i + 1
   if constexpr (KIND == 1) {
-#pragma unroll 4
-    for (int i = threadIdx.x; i < NT * (KS / 2) * 32; i += blockDim.x) {
-      const int ln = i & 31, h = (i >> 5) / (KS / 2) * 8 + (ln >> 2), ch = 32 * ((i >> 5) % (KS / 2)) + 8 * (ln & 3);
-      cp_async16(qs + i, static_cast<const uint16_t *>(a.q) + (h < G ? (head0 + h) * D + ch : 0), h < G);
+    const uint16_t *q0 = static_cast<const uint16_t *>(a.q);
+    const uint16_t *qp = q0 + (head0 + g) * D + 8 * c;  // a lane's column is the same in every fragment
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const bool ok = nt * 8 + g < G;
+#pragma unroll 3
+      for (int i = warp; i < KS / 2; i += warps)
+        cp_async16(qs + (nt * (KS / 2) + i) * 32 + lane, ok ? qp + nt * 8 * D + 32 * i : q0, ok);
     }
     cp_async_commit();
     for (int h = threadIdx.x; h < NT * 8; h += blockDim.x)
@@ -133,7 +137,7 @@ __global__ void __launch_bounds__(kWThreads) weights_mma_kernel(WeightsArgs a) {
     const int n0 = token_at(a, group, (tile + step) * 16 + g, n), n1 = token_at(a, group, (tile + step) * 16 + 8 + g, n);
     if constexpr (KIND == 1) {
       constexpr int NL = D / 32;              // 16-byte reads per row and lane
-      constexpr int U = NL < 6 ? NL : 6;      // rows of reads in flight
+      constexpr int U = NL < 6 ? NL : 6;      // pairs of reads in flight
       static_assert(NL % U == 0, "whole batches of reads");
 #pragma unroll
       for (int i0 = 0; i0 < NL; i0 += U) {
@@ -286,8 +290,8 @@ cudaError_t run_mma(const WeightsArgs &a, cudaStream_t st) {
       if (dev >= 0 && dev < 64) configured[dev] = true;
     }
   }
-  // resident CTAs an SM: five by registers, fewer where the latent's queries fill shared memory
-  const Split sp = split_of(a, 16, L::kBytes > 110 * 1024 ? 1 : L::kBytes > 70 * 1024 ? 3 : L::kBytes > 40 * 1024 ? 4 : 5);
+  // resident CTAs an SM, by registers (the latent's 128 heads: by shared memory)
+  const Split sp = split_of(a, 16, D == 576 ? (NT == 16 ? 1 : 2) : NT == 1 ? 5 : NT <= 4 ? 4 : 3);
   return launch_pdl(kern, dim3(sp.ctas, a.batch * a.n_kv_heads), dim3(sp.threads), L::kBytes, st, a);
 }
 
