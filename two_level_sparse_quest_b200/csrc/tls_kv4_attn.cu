@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
   // tokens past the end get zero scales, so that stale bytes stay finite.
   // Listed tokens come with cp.async, nine chunks of d / 8 bytes a record; where
   // some are missing, eight lanes bring a record's first eight chunks and every
-  // lane its own record's ninth, zero-filled.  (One bulk copy per listed record was slower:
-  // 24.0 us against 20.4 for 8 x 96k, 4096 tokens.)
+  // lane its own record's ninth, zero-filled.  (One bulk copy per listed record
+  // was slower: 24.0 us against 20.4 for 8 x 96k, 4096 tokens.)
   // The queries' loads go out first (warps below NT, one block of 8 heads each).
   uint4 qv[D / 32];
   if (warp < NT) {

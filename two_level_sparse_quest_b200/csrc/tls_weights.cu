@@ -16,6 +16,10 @@
 // queries sit in shared memory as B fragments, in the same order.  fp32 keys
 // take CUDA cores, four lanes a token.
 //
+// Measured (one B200): 64 groups of 4096 listed tokens, 4 heads, bf16 13.8 us
+// (5.1 TB/s), every token of 98304 268 us (6.2 TB/s); the latent's 64 heads over
+// 4 x 2048 tokens 8.1 us, most of it the 73 KB of queries that each SM fetches.
+//
 // The exponent is formed as tau s - lse in natural units, rounded once, before
 // it is scaled for exp2: the weights that matter have it near zero.  Each
 // token's sum over the heads has a fixed order and is added once, by one

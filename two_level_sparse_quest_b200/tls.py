@@ -330,7 +330,8 @@ def tls_kv4_attn_decode(shape, q, cache, out, lse_out=None, token_idx=None, seq_
                         n_slots=0, ws=None, stream=None):
     """Attention over a 4-bit cache: the tokens of token_idx, or without it every token below seq_lens."""
     wp, wb = _ws(ws)
-    pq, pc, pt, pn, ps, po, pl = _dptrs(q, cache, token_idx, seq_lens, slot_of_block, out, lse_out)
+    pq, pc, pt, pn, ps, po, pl, _ = _dptrs(q, cache, token_idx, seq_lens, slot_of_block, out, lse_out,
+                                           ws if isinstance(ws, torch.Tensor) else None)
     _check(_lib.tls_kv4_attn_decode(ctypes.byref(shape), pq, pc, pt, pn, ps, int(n_slots), po, pl, wp, wb,
                                     _stream(stream)), "tls_kv4_attn_decode")
 
