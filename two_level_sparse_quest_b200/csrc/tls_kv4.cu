@@ -163,9 +163,18 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(Kv4RowsArgs a) 
     const int log_r = 31 - __clz(a.n_label);  // a power of two
     const int l = tid & (a.n_label - 1), k = a.label_idx[l];
     const bool ok = k >= 0 && k < D;
-    for (int t = t_begin + (tid >> log_r); t < t_end; t += kRowThreads >> log_r)
-      slab[(static_cast<size_t>(t - t_begin) << log_r) + l] =
-          ok ? K[static_cast<size_t>(t - old_len) * D + k] : static_cast<uint16_t>(0);
+    const int rows = kRowThreads >> log_r;
+    for (int t0 = t_begin + (tid >> log_r); t0 < t_end; t0 += 4 * rows) {
+      uint16_t v[4];  // the loads first: one round trip
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int t = t0 + u * rows;
+        v[u] = ok && t < t_end ? K[static_cast<size_t>(t - old_len) * D + k] : static_cast<uint16_t>(0);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (t0 + u * rows < t_end) slab[(static_cast<size_t>(t0 + u * rows - t_begin) << log_r) + l] = v[u];
+    }
   }
 }
 
