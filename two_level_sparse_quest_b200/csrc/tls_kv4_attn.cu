@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
 #pragma unroll
   for (int s = 0; s < kRing; ++s) valid[s] = 0;
   // rows of the next two tiles: their ids are on the way while earlier tiles are copied and computed
-  int row_next = row_of(t_issue), row_after = row_of(t_issue + stride), stage_issue = 0;
+  int row_next = kBulk ? 0 : row_of(t_issue), row_after = kBulk ? 0 : row_of(t_issue + stride), stage_issue = 0;
   if constexpr (kBulk) {
     if (lane == 0) {
 #pragma unroll
@@ -192,17 +192,25 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
     __syncwarp();
   }
   auto issue = [&]() -> uint32_t {
-    const int row = row_next;
-    const uint32_t mask = __ballot_sync(0xffffffffu, row >= 0);
-    if (mask != 0u) {
-      if constexpr (kBulk) {
-        uint64_t *bar = &s_full[warp][stage_issue];
-        if (lane == 0) mbarrier_expect_tx(bar, __popc(mask) * R::kBytes);
-        if (lane == 0)
-          bulk_load(ring + stage_issue * L::kStage, base + static_cast<size_t>(row) * R::kBytes, __popc(mask) * R::kBytes, bar);
-        if (mask != 0xffffffffu && row < 0)  // the last stage of all: nothing is copied over these zeros
-          *reinterpret_cast<uint4 *>(ring + stage_issue * L::kStage + lane * R::kBytes + R::kKS) = make_uint4(0u, 0u, 0u, 0u);
-      } else {
+    uint32_t mask;
+    if constexpr (kBulk) {
+      const int left = t_issue < t_end ? n - t_issue * kTile : 0;  // tokens of this stage, at least; the same in every lane
+      mask = left >= kTile ? 0xffffffffu : (1u << max(left, 0)) - 1u;
+      if (left > 0) {
+        unsigned char *dst = ring + stage_issue * L::kStage;
+        if (lane == 0) {
+          const uint32_t bytes = min(left, kTile) * R::kBytes;
+          mbarrier_expect_tx(&s_full[warp][stage_issue], bytes);
+          bulk_load(dst, base + static_cast<size_t>(t_issue) * (kTile * R::kBytes), bytes, &s_full[warp][stage_issue]);
+        }
+        if (lane >= left)  // the last stage of all: nothing is copied over these zeros
+          *reinterpret_cast<uint4 *>(dst + lane * R::kBytes + R::kKS) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      t_issue += stride;
+    } else {
+      const int row = row_next;
+      mask = __ballot_sync(0xffffffffu, row >= 0);
+      if (mask != 0u) {
         constexpr int CB = R::kChunk;
         const uint32_t dst = ring_s + stage_issue * L::kStage;
         if (mask == 0xffffffffu) {
@@ -224,10 +232,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
                              row >= 0 ? base + static_cast<long long>(row) * R::kBytes + 8 * CB : base, row >= 0);
         }
       }
+      t_issue += stride;
+      row_next = row_after;
+      row_after = row_of(t_issue + stride);
     }
-    t_issue += stride;
-    row_next = row_after;
-    row_after = row_of(t_issue + stride);
     if (++stage_issue == kRing) stage_issue = 0;
     return mask;
   };
@@ -291,7 +299,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
   const int vtok0 = 2 * row_token(2 * c), vtok1 = 2 * row_token(2 * c + 1);
 
   int st = 0;
-  uint32_t phases = 0;  // mbarrier parity of each stage
+  uint32_t phase = 0;  // mbarrier parity of the ring's current round (every stage is used once a round until the last tile)
   bool alive = true;
   for (int it = 0; it < my_tiles; ++it) {
 #pragma unroll
@@ -305,9 +313,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
     const uint32_t vm = valid[0];
     if constexpr (kBulk) {
       if (vm != 0u) {  // a wait that gives up (which a correct run never sees): no further copies, the result is undefined
-        if (!mbarrier_wait(&s_full[warp][st], (phases >> st) & 1u)) alive = false;
-        phases ^= 1u << st;
-        if (!__all_sync(0xffffffffu, alive)) {
+        const bool arrived = mbarrier_wait(&s_full[warp][st], phase);
+        if (!__all_sync(0xffffffffu, arrived)) {
           alive = false;
           if (lane == 0 && a.err) atomicOr(a.err, kErrAttnWait);
         }
@@ -458,7 +465,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
       }
     }
     __syncwarp();
-    if (++st == kRing) st = 0;
+    if (++st == kRing) {
+      st = 0;
+      phase ^= 1u;
+    }
   }
   if constexpr (!kBulk) cp_async_wait<0>();
   __syncwarp();
