@@ -362,3 +362,71 @@ def test_decode_loop_over_a_4bit_cache_with_eviction(T):
                 mirror_w[b, h] = got_w[b, h]
                 assert (np.abs(got_w[b, h] - (prev + add)) <= wtol + R.U32 * (prev + add)).all()
     assert evictions >= 1 and (mirror[:, :, :min(lens)] == cache.cpu().numpy()[:, :, :min(lens)]).mean() > 0.999
+
+
+def test_captured_upkeep_replays(T):
+    """Append, attention, weights, selection and compaction captured in one graph and replayed on new inputs give the
+    bits of the eager calls."""
+    rng = np.random.default_rng(5)
+    B, H, G, d, ctx, budget = 2, 2, 4, 64, 1200, 700
+    s = make(T, B, H, G, d, ctx)
+    start = torch.from_numpy(R.records(rng.standard_normal((B, H, ctx, d)), rng.standard_normal((B, H, ctx, d)))).cuda()
+    w_start = torch.rand((B, H, ctx), device="cuda")
+    K, V, q = (torch.zeros(sh, dtype=BF16, device="cuda") for sh in ((B, H, 1, d), (B, H, 1, d), (B, H * G, d)))
+    old, new = i32([1100, 900]), i32([1101, 901])
+    ws = torch.empty(T.tls_kv4_workspace_size(s), dtype=torch.uint8, device="cuda")
+    cache, w = start.clone(), w_start.clone()
+    out, lse = torch.zeros((B, H * G, d), device="cuda"), torch.zeros((B, H * G), device="cuda")
+    keep, lens = torch.zeros((B, H, budget), dtype=torch.int32, device="cuda"), i32([0, 0])
+    back = torch.zeros((B, H, ctx, d), dtype=BF16, device="cuda")
+
+    def step():
+        T.tls_kv4_append(s, K, V, old, new, 1, cache)
+        T.tls_kv4_attn_decode(s, q, cache, out, lse, seq_lens=new, ws=ws)
+        T.tls_kv4_accum_weights(s, q, cache, lse, w, seq_lens=new)
+        T.tls_evict_select(s, budget, 4, 32, w, new, keep, lens)
+        T.tls_evict_compact(s, budget, keep, new, [cache], w)
+        T.tls_kv4_read(s, cache, i0, lens, ctx, back)
+
+    i0 = i32([0, 0])
+
+    def fresh(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        for x in (K, V, q):
+            x.copy_(torch.randn(x.shape, generator=g, device="cuda"))
+        cache.copy_(start)
+        w.copy_(w_start)
+        for x in (out, lse, keep, lens, back):
+            x.zero_()
+
+    def outputs():
+        torch.cuda.synchronize()
+        return [x.clone() for x in (cache, w, out, lse, keep, lens, back)]
+
+    want = []
+    for seed in (1, 2):
+        fresh(seed)
+        step()
+        want.append(outputs())
+    graph = torch.cuda.CUDAGraph()
+    fresh(3)
+    with torch.cuda.graph(graph):
+        step()
+    for seed, ref in ((2, want[1]), (1, want[0]), (2, want[1])):
+        fresh(seed)
+        graph.replay()
+        for a, b in zip(outputs(), ref):
+            assert torch.equal(a, b)
+    assert T.tls_device_error(clear=True) == 0
+
+
+def test_compact_weights_alone(T):
+    s = make(T, 1, 2, 1, 64, 50)
+    w0 = torch.rand((1, 2, 50), device="cuda") + 1
+    w = w0.clone()
+    keep = i32([[[1, 4, 30, -1], [0, 1, 2, 44]]])
+    T.tls_evict_compact(s, 4, keep, i32([45]), [], w)
+    want = w0.clone()
+    want[:, :, :45] = 0
+    want[0, 0, :3], want[0, 1, :4] = w0[0, 0, [1, 4, 30]], w0[0, 1, [0, 1, 2, 44]]
+    assert torch.equal(w, want)

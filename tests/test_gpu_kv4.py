@@ -463,3 +463,22 @@ def test_prefetched_blocks_are_attended(T, d, bs):
                 held[b][h] = set(sel[b][h])
         prev = nxt
     assert T.tls_device_error(clear=True) == 0
+
+
+def test_attention_many_groups_and_clamped_lengths(T):
+    rng = np.random.default_rng(17)
+    check_attention(T, 70, 3, 2, 64, 60, lists(rng, 70, 3, 60, 35, pad=1), "list", out_dtype=1)
+    check_attention(T, 2, 1, 32, 128, 9001, [9001, 4500], "dense", out_dtype=1)  # two units a group, cut into parts
+    # lengths outside [0, max_ctx] are clamped: compared with the clamped ones
+    d, ctx = 128, 333
+    s = shape(T, 3, 1, 4, d, ctx)
+    rec = torch.from_numpy(R.records(rng.standard_normal((3, 1, ctx, d)), rng.standard_normal((3, 1, ctx, d)))).cuda()
+    q = bf16_rows(rng, (3, 4, d), 1.0, False).cuda()
+    ws = torch.zeros(T.tls_kv4_workspace_size(s), dtype=torch.uint8, device="cuda")
+    got = []
+    for lens in ([-3, 2 ** 31 - 1, 5], [0, ctx, 5]):
+        out, lse = torch.full((3, 4, d), 7.0, device="cuda"), torch.full((3, 4), 7.0, device="cuda")
+        T.tls_kv4_attn_decode(s, q, rec, out, lse, seq_lens=i32(lens), ws=ws)
+        got.append((out, lse))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert not got[0][0][0].any() and (got[0][1][0] == -float("inf")).all()
