@@ -26,7 +26,7 @@ def fake_cuda(index):
 
 
 def test_tensors_of_another_device_are_refused(T, monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(T, "_current_device", lambda: 1)
     here, there = fake_cuda(1), fake_cuda(0)
     assert T._dptrs(here, None, 0x20, here) == [0x1100, None, 0x20, 0x1100]
     for args in ((there,), (here, there), (there, here)):

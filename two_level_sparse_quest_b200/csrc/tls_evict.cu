@@ -368,7 +368,7 @@ cudaError_t launch_evict_select(const EvictArgs &a, cudaStream_t st) {
   while (cs < kMaxCluster && static_cast<long long>(cs) * 4096 < a.max_ctx &&
          static_cast<long long>(groups) * cs * 2 <= a.num_sms)
     cs *= 2;
-  const long long slice = ((static_cast<long long>(a.max_ctx) + cs - 1) / cs + 31) / 32 * 32;
+  const long long slice = ((static_cast<long long>(a.max_ctx) + cs - 1) / cs + 127) / 128 * 128;
   const int cap = static_cast<int>(std::min<long long>(slice, kSelCap));
   const size_t smem = static_cast<size_t>(cap) * 4;
   static bool configured[64] = {};

@@ -8,7 +8,9 @@
 // Bound: a token is 9 d / 8 bytes (144 at d 128), against 4 G d flop, so HBM
 // is the floor; at that rate an SM has 6.4 cycles for a token, and it is the
 // instructions that widen the codes (two for each pair of channels: e2m1 ->
-// fp16, times the scale) that come near it, not the tensor pipe.
+// fp16, times the scale, each at half rate) that come near it, not the tensor
+// pipe.  Measured (one B200): 64 groups of 98304 tokens, 4 heads, 170 us (5.3
+// TB/s, 0.81 of the measured copy rate); of 4096 listed ones 19.8 us.
 //
 // Layout: the tokens are the MMA rows.  S^T[16 tokens x 8 heads] = K q^T takes
 // one m16n8k16 per 16 channels, O^T[16 channels x 8 heads] += V^T P^T one per
@@ -322,7 +324,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
     }
     if (vm != 0u && alive) {
       const unsigned char *S = ring + st * L::kStage;
-#pragma unroll NT == 1 ? 2 : 1
+      // (both halves in one body where the registers allow it: a slot cache's lookup leaves too few, 9.0 us against 8.6)
+#pragma unroll NT == 1 && !PAGED ? 2 : 1
       for (int hf = 0; hf < 2; ++hf, S += R::kBytes) {  // even tokens of the stage, then odd ones
         // ---- S^T = K q^T: rows g, g + 8 of heads 2c, 2c + 1
         float s[NT][4];
@@ -343,24 +346,30 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
           sc0 = k0[R::kKS + c];
           sc1 = k1[R::kKS + c];
         }
+        // a word is widened while the one before it is scaled and multiplied: the three take different pipes
+        uint32_t x[2][4], y[2][4];
+        auto widen = [&](int w) {
+          e2m1_unpack(w0[w], x[w & 1][0], x[w & 1][1], x[w & 1][2], x[w & 1][3]);
+          e2m1_unpack(w1[w], y[w & 1][0], y[w & 1][1], y[w & 1][2], y[w & 1][3]);
+        };
+        widen(0);
 #pragma unroll
         for (int w = 0; w < CW; ++w) {
+          if (w + 1 < CW) widen(w + 1);
           // words 0, 1 of a row lie in the lane's first group of 16 channels, 2, 3 in its second
           const uint32_t f0 = (w < 2 ? sc0 & 0xffu : sc0 >> 8) * 0x00800080u;
           const uint32_t f1 = (w < 2 ? sc1 & 0xffu : sc1 >> 8) * 0x00800080u;
-          uint32_t x[4], y[4];
-          e2m1_unpack(w0[w], x[0], x[1], x[2], x[3]);
-          e2m1_unpack(w1[w], y[0], y[1], y[2], y[3]);
+          uint32_t (&X)[4] = x[w & 1], (&Y)[4] = y[w & 1];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            x[e] = hmul2(x[e], f0);
-            y[e] = hmul2(y[e], f1);
+            X[e] = hmul2(X[e], f0);
+            Y[e] = hmul2(Y[e], f1);
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const uint4 qv = s_q[nt][w][lane];
-            mma_f16(s[nt], x[0], y[0], x[1], y[1], qv.x, qv.y);
-            mma_f16(s[nt], x[2], y[2], x[3], y[3], qv.z, qv.w);
+            const uint4 qf = s_q[nt][w][lane];
+            mma_f16(s[nt], X[0], Y[0], X[1], Y[1], qf.x, qf.y);
+            mma_f16(s[nt], X[2], Y[2], X[3], Y[3], qf.z, qf.w);
           }
         }
         // ---- online softmax in the log2 domain: t = score - m + 14
@@ -650,7 +659,7 @@ int max_parts(int sms) { return 4 * sms; }
 // for a tile when two CTAs share an SM and 1.1 us alone; a wave of CTAs costs
 // 3.5 us around its tiles, a cluster 1 us, the second launch 3.  Measured:
 // 64 units of 4096 tokens 19.8 us with clusters of 4 (one wave), 22.0 with 2,
-// 25.5 with 8 (two waves), 27 as 9 parts; 64 units of 98304 tokens 172 us as 9
+// 25.5 with 8 (two waves), 27 as 9 parts; 64 units of 98304 tokens 170 us as 9
 // parts (two full waves), 184 with clusters of 4, 211 with 8.
 void kv4_plan(Kv4AttnArgs &a, int n_max) {
   const int G = a.n_q_heads / a.n_kv_heads;

@@ -142,17 +142,25 @@ def _dptr(x):
     return _ptr(x)
 
 
+# The plain forms of torch.cuda.current_device() and torch.cuda.current_stream().cuda_stream: the objects that those
+# build cost a call 3 us.
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _dptrs(*xs):
     """_dptr of several arguments, whose tensors must lie on the current device
     (the one that the call launches on)."""
     cur, out = -2, []
     for x in xs:
-        if isinstance(x, torch.Tensor):
+        if x is None:
+            out.append(None)
+        elif isinstance(x, torch.Tensor):
             dev = x.get_device()  # -1: host memory
             if dev != cur:
                 if dev < 0:
                     raise ValueError("expected a CUDA tensor (the kernels address device memory)")
-                cur = torch.cuda.current_device()
+                cur = _current_device()
                 if dev != cur:
                     raise ValueError(f"tensor on cuda:{dev}, but the current device is cuda:{cur}")
             if not x.is_contiguous():
@@ -172,9 +180,8 @@ def _hptr(x):
 
 def _stream(stream):
     if stream is None:
-        # the handle alone: a torch.cuda.Stream object costs 3 us a call
         if torch.cuda.is_initialized():
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+            return _raw_stream(_current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -329,9 +336,12 @@ def tls_kv4_read(shape, cache, old_lens, new_lens, row_stride, K_out=None, V_out
 def tls_kv4_attn_decode(shape, q, cache, out, lse_out=None, token_idx=None, seq_lens=None, slot_of_block=None,
                         n_slots=0, ws=None, stream=None):
     """Attention over a 4-bit cache: the tokens of token_idx, or without it every token below seq_lens."""
-    wp, wb = _ws(ws)
-    pq, pc, pt, pn, ps, po, pl, _ = _dptrs(q, cache, token_idx, seq_lens, slot_of_block, out, lse_out,
-                                           ws if isinstance(ws, torch.Tensor) else None)
+    if isinstance(ws, torch.Tensor):
+        wb = ws.nbytes
+        wp, pq, pc, pt, pn, ps, po, pl = _dptrs(ws, q, cache, token_idx, seq_lens, slot_of_block, out, lse_out)
+    else:
+        wp, wb = _ws(ws)
+        pq, pc, pt, pn, ps, po, pl = _dptrs(q, cache, token_idx, seq_lens, slot_of_block, out, lse_out)
     _check(_lib.tls_kv4_attn_decode(ctypes.byref(shape), pq, pc, pt, pn, ps, int(n_slots), po, pl, wp, wb,
                                     _stream(stream)), "tls_kv4_attn_decode")
 
