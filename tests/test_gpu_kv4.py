@@ -482,3 +482,26 @@ def test_attention_many_groups_and_clamped_lengths(T):
         got.append((out, lse))
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
     assert not got[0][0][0].any() and (got[0][1][0] == -float("inf")).all()
+
+
+def test_summary_of_special_values(T):
+    """Signed zeros, infinities, NaN and a column that holds nothing else: the summary's bits are a full build's,
+    whether the rows come at once or one by one."""
+    d, n, bs = 64, 24, 8
+    x = np.random.default_rng(2).standard_normal((n, d)).astype(np.float32)
+    x[:, 0], x[::2, 1], x[1::2, 1] = np.nan, 0.0, -0.0
+    x[:, 2], x[5, 3], x[6, 3], x[7, 4] = -0.0, np.inf, -np.inf, np.nan
+    K = torch.from_numpy(x).to(BF16)[None, None].cuda()
+    s = shape(T, 1, 1, 2, d, n, bs)
+    label = i32(list(range(16)))
+    want = [torch.zeros((1, 1, n // bs, 2, d), dtype=BF16, device="cuda"), torch.zeros((1, 1, n, 16), dtype=BF16, device="cuda")]
+    T.tls_build_block_meta(s, K, i32([n]), label, *want)
+    for step in (n, 5, 1):
+        got = [torch.zeros_like(w) for w in want]
+        cache = torch.zeros((1, 1, n, 72), dtype=torch.uint8, device="cuda")
+        for t in range(0, n, step):
+            e = min(n, t + step)
+            rows = K[:, :, t:e].contiguous()
+            T.tls_kv4_append(s, rows, rows, i32([t]), i32([e]), e - t, cache, label, *got)
+        for g, w in zip(got, want):
+            assert torch.equal(g.view(torch.int16), w.view(torch.int16)), step

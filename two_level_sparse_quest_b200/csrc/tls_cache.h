@@ -33,7 +33,7 @@ struct Kv4AttnArgs {
   int batch, n_q_heads, n_kv_heads, d, block_size, n_blocks_max, max_ctx, k_t, out_dtype;
   float scale_log2;
   int num_sms;
-  int head_chunk, n_head_chunks, cluster, n_split;  // Kv4Plan
+  int head_chunk, n_head_chunks, cluster, n_split;  // set by the launch (kv4_plan)
 };
 size_t kv4_attn_part_floats(int heads_per_group, int d, int num_sms);  // workspace floats of any call
 cudaError_t launch_kv4_attention(Kv4AttnArgs a, cudaStream_t st);
