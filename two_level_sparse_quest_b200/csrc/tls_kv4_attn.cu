@@ -9,8 +9,8 @@
 // is the floor; at that rate an SM has 6.4 cycles for a token, and it is the
 // instructions that widen the codes (two for each pair of channels: e2m1 ->
 // fp16, times the scale, each at half rate) that come near it, not the tensor
-// pipe.  Measured (one B200): 64 groups of 98304 tokens, 4 heads, 170 us (5.3
-// TB/s, 0.81 of the measured copy rate); of 4096 listed ones 19.8 us.
+// pipe.  Measured (one B200): 64 groups of 98304 tokens, 4 heads, 168 us (5.4
+// TB/s, 0.82 of the measured copy rate); of 4096 listed ones 19.7 us.
 //
 // Layout: the tokens are the MMA rows.  S^T[16 tokens x 8 heads] = K q^T takes
 // one m16n8k16 per 16 channels, O^T[16 channels x 8 heads] += V^T P^T one per
@@ -95,9 +95,9 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   return r;
 }
 
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+__device__ __forceinline__ float2 ld_cluster(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
   return v;
 }
 
@@ -116,8 +116,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
   constexpr int VW = D / 64;   // 32-bit words of V codes per lane and token
   constexpr bool kBulk = !LIST && R::kBytes % 16 == 0;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ float s_ml[kWarps][8 * NT][2];
-  __shared__ float s_cta[8 * NT][2];
+  __shared__ __align__(8) float s_ml[kWarps][8 * NT][2];
+  __shared__ __align__(8) float s_cta[8 * NT][2];
   __shared__ uint4 s_q[NT][D / 32][32];
   __shared__ float s_scale[8 * NT];
   __shared__ uint64_t s_full[kWarps][kRing];
@@ -324,8 +324,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
     }
     if (vm != 0u && alive) {
       const unsigned char *S = ring + st * L::kStage;
-      // (both halves in one body where the registers allow it: a slot cache's lookup leaves too few, 9.0 us against 8.6)
-#pragma unroll NT == 1 && !PAGED ? 2 : 1
+      // (both halves in one body where the registers allow it: a list's copies leave too few, 19.9 us against 19.7)
+#pragma unroll NT == 1 && !LIST ? 2 : 1
       for (int hf = 0; hf < 2; ++hf, S += R::kBytes) {  // even tokens of the stage, then odd ones
         // ---- S^T = K q^T: rows g, g + 8 of heads 2c, 2c + 1
         float s[NT][4];
@@ -504,27 +504,31 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
   }
   __syncthreads();
 
-  // ---- joined over the CTA's warps (a warp without a token has m = -inf, l = 0)
+  // ---- joined over the CTA's warps (a warp without a token has m = -inf, l = 0), two channels a thread
   float *cta_o = reinterpret_cast<float *>(smem);
-  const int n_out = HG * D;
-  for (int i = threadIdx.x; i < n_out; i += kWarps * 32) {
-    const int h = i / D, ch = i % D;
+  const int n_pairs = HG * (D / 2);
+  for (int i = threadIdx.x; i < n_pairs; i += kWarps * 32) {
+    const int h = i / (D / 2), ch = 2 * (i % (D / 2));
+    float2 ml[kWarps], ow[kWarps];
     float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w][h][0]);
+    for (int w = 0; w < kWarps; ++w) {
+      ml[w] = *reinterpret_cast<const float2 *>(s_ml[w][h]);
+      ow[w] = *reinterpret_cast<const float2 *>(reinterpret_cast<const float *>(smem + w * L::kWarpBytes) + L::at(h, ch));
+      M = fmaxf(M, ml[w].x);
+    }
     const float Mu = M == -INFINITY ? 0.f : M;
-    float acc = 0.f, ls = 0.f;
+    float ls = 0.f;
+    float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = ex2(s_ml[w][h][0] - Mu);
-      ls = fmaf(f, s_ml[w][h][1], ls);
-      acc = fmaf(f, reinterpret_cast<const float *>(smem + w * L::kWarpBytes)[L::at(h, ch)], acc);
+      const float f = ex2(ml[w].x - Mu);
+      ls = fmaf(f, ml[w].y, ls);
+      acc.x = fmaf(f, ow[w].x, acc.x);
+      acc.y = fmaf(f, ow[w].y, acc.y);
     }
-    cta_o[L::at(h, ch)] = acc;  // warp 0's element (h, ch): read by this thread only
-    if (ch == 0) {
-      s_cta[h][0] = M;
-      s_cta[h][1] = ls;
-    }
+    *reinterpret_cast<float2 *>(cta_o + L::at(h, ch)) = acc;  // warp 0's elements (h, ch ..): read by this thread only
+    if (ch == 0) *reinterpret_cast<float2 *>(s_cta[h]) = make_float2(M, ls);
   }
   if (CS > 1) {
     cluster_arrive_release();
@@ -535,46 +539,49 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
 
   // ---- joined over the cluster: each CTA writes a share of the outputs
   const size_t n_units = static_cast<size_t>(a.batch) * a.n_kv_heads * a.n_head_chunks;
-  for (int i = rank * (kWarps * 32) + threadIdx.x; i < n_out; i += CS * kWarps * 32) {
-    const int h = i / D, ch = i % D;
-    float M, ls, acc;
+  const int share = (n_pairs + CS - 1) / CS, i_end = min(n_pairs, (rank + 1) * share);
+  for (int i = rank * share + threadIdx.x; i < i_end; i += kWarps * 32) {
+    const int h = i / (D / 2), ch = 2 * (i % (D / 2));
+    float M, ls;
+    float2 acc;
     if (CS == 1) {
-      M = s_cta[h][0];
-      ls = s_cta[h][1];
-      acc = cta_o[L::at(h, ch)];
+      const float2 t = *reinterpret_cast<const float2 *>(s_cta[h]);
+      M = t.x;
+      ls = t.y;
+      acc = *reinterpret_cast<const float2 *>(cta_o + L::at(h, ch));
     } else {
-      const uint32_t am = smem_addr(&s_cta[h][0]), ao = smem_addr(cta_o + L::at(h, ch));
-      float mr[kMaxCluster], lr[kMaxCluster], orr[kMaxCluster];
+      const uint32_t am = smem_addr(s_cta[h]), ao = smem_addr(cta_o + L::at(h, ch));
+      float2 mr[kMaxCluster], orr[kMaxCluster];  // all loads first: one round trip
       M = -INFINITY;
 #pragma unroll
       for (int r = 0; r < kMaxCluster; ++r) {
-        mr[r] = r < CS ? ld_cluster(cluster_map(am, r)) : -INFINITY;
-        lr[r] = r < CS ? ld_cluster(cluster_map(am, r) + 4) : 0.f;
-        orr[r] = r < CS ? ld_cluster(cluster_map(ao, r)) : 0.f;
-        M = fmaxf(M, mr[r]);
+        mr[r] = r < CS ? ld_cluster(cluster_map(am, r)) : make_float2(-INFINITY, 0.f);
+        orr[r] = r < CS ? ld_cluster(cluster_map(ao, r)) : make_float2(0.f, 0.f);
       }
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) M = fmaxf(M, mr[r].x);
       const float Mu = M == -INFINITY ? 0.f : M;
-      ls = acc = 0.f;
+      ls = 0.f;
+      acc = make_float2(0.f, 0.f);
 #pragma unroll
       for (int r = 0; r < kMaxCluster; ++r) {
-        const float f = ex2(mr[r] - Mu);
-        ls = fmaf(f, lr[r], ls);
-        acc = fmaf(f, orr[r], acc);
+        const float f = ex2(mr[r].x - Mu);
+        ls = fmaf(f, mr[r].y, ls);
+        acc.x = fmaf(f, orr[r].x, acc.x);
+        acc.y = fmaf(f, orr[r].y, acc.y);
       }
     }
     if (a.n_split > 1) {
       float *ml = a.part + (static_cast<size_t>(unit) * a.n_split + part) * HG * 2;
-      float *pp = a.part + n_units * a.n_split * HG * 2 + (static_cast<size_t>(unit) * a.n_split + part) * n_out;
-      pp[i] = acc;
-      if (ch == 0) {
-        ml[2 * h] = M;
-        ml[2 * h + 1] = ls;
-      }
+      float *pp = a.part + n_units * a.n_split * HG * 2 + (static_cast<size_t>(unit) * a.n_split + part) * HG * D;
+      *reinterpret_cast<float2 *>(pp + 2 * i) = acc;
+      if (ch == 0) *reinterpret_cast<float2 *>(ml + 2 * h) = make_float2(M, ls);
     } else {
-      const float res = ls == 0.f ? 0.f : acc / ls;
+      const float2 res = ls == 0.f ? make_float2(0.f, 0.f) : make_float2(acc.x / ls, acc.y / ls);
       const size_t head = static_cast<size_t>(b) * a.n_q_heads + head0 + h;
-      if (a.out_dtype == 1) static_cast<__nv_bfloat16 *>(a.out)[head * D + ch] = __float2bfloat16_rn(res);
-      else static_cast<float *>(a.out)[head * D + ch] = res;
+      if (a.out_dtype == 1)
+        *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) + head * D + ch) = __floats2bfloat162_rn(res.x, res.y);
+      else *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + head * D + ch) = res;
       if (a.lse && ch == 0) a.lse[head] = ls == 0.f ? -INFINITY : (M + (log2f(ls) - kPShift)) * 0.69314718055994531f;
     }
   }
@@ -658,8 +665,8 @@ int max_parts(int sms) { return 4 * sms; }
 // microsecond (fitted at d 128, 4 heads) finds cheaper.  A warp takes 1.9 us
 // for a tile when two CTAs share an SM and 1.1 us alone; a wave of CTAs costs
 // 3.5 us around its tiles, a cluster 1 us, the second launch 3.  Measured:
-// 64 units of 4096 tokens 19.8 us with clusters of 4 (one wave), 22.0 with 2,
-// 25.5 with 8 (two waves), 27 as 9 parts; 64 units of 98304 tokens 170 us as 9
+// 64 units of 4096 tokens 19.7 us with clusters of 4 (one wave), 22.0 with 2,
+// 25.5 with 8 (two waves), 27 as 9 parts; 64 units of 98304 tokens 168 us as 9
 // parts (two full waves), 184 with clusters of 4, 211 with 8.
 void kv4_plan(Kv4AttnArgs &a, int n_max) {
   const int G = a.n_q_heads / a.n_kv_heads;
