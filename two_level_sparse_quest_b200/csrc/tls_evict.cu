@@ -18,12 +18,13 @@
 //   one bin.
 // compact: row keep[j] moves to row j.  As keep ascends, a chunk of rows only
 //   overwrites rows that no later chunk reads, so chunk by chunk -- all loads,
-//   a barrier, all stores -- is in place without a copy.  A cluster takes a
-//   column slice of one array of one group and a super-chunk of rows at a
-//   time, so a single sequence still fills the GPU.
+//   a barrier, all stores -- is in place without a copy.  A CTA takes a column
+//   slice of one array of one group; where such slices are few, a cluster takes
+//   it, a chunk for each of its CTAs at a time, so that a single sequence still
+//   fills the GPU.
 // Both are bound by HBM: 4 bytes a token, and each kept row once in and out.
-// Half of 8 x 8 caches of 98304 tokens, K and V in bf16: 613 us in all, the
-// selection 28 of them (the moves 5.7 TB/s); one sequence of 49152 tokens in 4
+// Half of 8 x 8 caches of 98304 tokens, K and V in bf16: 569 us in all, the
+// selection 28 of them (the moves 6.0 TB/s); one sequence of 49152 tokens in 4
 // bits 34 us, the selection 15.
 #include <algorithm>
 
@@ -275,10 +276,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, 
 }
 
 // ---------------------------------------------------------------- compact
-constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 8;
 
-template <typename V>
+template <typename V, int kMoveThreads>
 __device__ void move_rows(const CompactArgs &a, int arr, int vec0, int n_vec, int group, int len, int rank, int CS) {
   // columns vec0 .. vec0 + n_vec - 1 (in units of V) of array arr
   const size_t row_vecs = a.row_bytes[arr] / sizeof(V);
@@ -338,7 +338,8 @@ struct MovePlan {
   int cluster;
 };
 
-__global__ void __launch_bounds__(kMoveThreads, 3) evict_compact_kernel(CompactArgs a, MovePlan p) {
+template <int kMoveThreads>
+__global__ void __launch_bounds__(kMoveThreads, kMoveThreads == 256 ? 3 : 1) evict_compact_kernel(CompactArgs a, MovePlan p) {
   grid_dependency_wait();
   const int CS = p.cluster;
   const int rank = static_cast<int>(blockIdx.x) % CS, slice = static_cast<int>(blockIdx.x) / CS;
@@ -350,11 +351,11 @@ __global__ void __launch_bounds__(kMoveThreads, 3) evict_compact_kernel(CompactA
   const int vec0 = (slice - p.first[arr]) * p.slice[arr];
   const int n_vec = min(p.slice[arr], a.row_bytes[arr] / vb - vec0);
   switch (vb) {
-    case 16: move_rows<uint4>(a, arr, vec0, n_vec, group, len, rank, CS); break;
-    case 8: move_rows<uint2>(a, arr, vec0, n_vec, group, len, rank, CS); break;
-    case 4: move_rows<uint32_t>(a, arr, vec0, n_vec, group, len, rank, CS); break;
-    case 2: move_rows<uint16_t>(a, arr, vec0, n_vec, group, len, rank, CS); break;
-    default: move_rows<uint8_t>(a, arr, vec0, n_vec, group, len, rank, CS); break;
+    case 16: move_rows<uint4, kMoveThreads>(a, arr, vec0, n_vec, group, len, rank, CS); break;
+    case 8: move_rows<uint2, kMoveThreads>(a, arr, vec0, n_vec, group, len, rank, CS); break;
+    case 4: move_rows<uint32_t, kMoveThreads>(a, arr, vec0, n_vec, group, len, rank, CS); break;
+    case 2: move_rows<uint16_t, kMoveThreads>(a, arr, vec0, n_vec, group, len, rank, CS); break;
+    default: move_rows<uint8_t, kMoveThreads>(a, arr, vec0, n_vec, group, len, rank, CS); break;
   }
 }
 
@@ -389,9 +390,7 @@ cudaError_t launch_evict_compact(const CompactArgs &a, cudaStream_t st) {
   const int sms = a.num_sms > 0 ? a.num_sms : 148;
   // Column slices of whole rows up to 256 bytes, or narrower (64 bytes at
   // least) while clusters of eight do not reach two CTAs an SM; then the
-  // largest cluster with which all CTAs run at once, three an SM.  64 groups,
-  // K and V of 256-byte rows: 617 us; slices of 128 bytes 625, of 64 bytes 638
-  // at their best cluster size, 700 to 850 where the last wave is part empty.
+  // largest cluster with which all CTAs run at once, three an SM.
   int slices = 0;
   for (int wide = 256; wide >= 64; wide /= 2) {
     slices = 0;
@@ -403,17 +402,25 @@ cudaError_t launch_evict_compact(const CompactArgs &a, cudaStream_t st) {
       const int vecs = a.row_bytes[i] / v;
       const int n_slices = (a.row_bytes[i] + wide - 1) / wide;
       p.vec_bytes[i] = v;
-      p.slice[i] = std::min((vecs + n_slices - 1) / n_slices, kMoveThreads);
+      p.slice[i] = std::min((vecs + n_slices - 1) / n_slices, 256);
       p.first[i] = slices;
       slices += (vecs + p.slice[i] - 1) / p.slice[i];
     }
     if (static_cast<long long>(groups) * slices * kMaxCluster >= 2 * sms) break;
   }
   p.first[a.n_rows] = slices;
+  // Slices that nearly fill the SMs by themselves take a large CTA each: its
+  // barrier is cheaper than a cluster's (64 groups 568 us against 613, 48
+  // groups 462 against 547; with 32 groups, 96 slices, 390 against 356).
+  const long long units = static_cast<long long>(groups) * slices;
+  if (units * 5 >= 4LL * sms) {
+    p.cluster = 1;
+    return launch_pdl(evict_compact_kernel<512>, dim3(slices, groups), dim3(512), 0, st, a, p);
+  }
   int cs = 1;
-  while (cs < kMaxCluster && static_cast<long long>(groups) * slices * cs * 2 <= 3 * sms) cs *= 2;
+  while (cs < kMaxCluster && units * cs * 2 <= 3 * sms) cs *= 2;
   p.cluster = cs;
-  return launch_pdl_cluster(evict_compact_kernel, dim3(slices * cs, groups), dim3(kMoveThreads), 0, st, cs, a, p);
+  return launch_pdl_cluster(evict_compact_kernel<256>, dim3(slices * cs, groups), dim3(256), 0, st, cs, a, p);
 }
 
 }  // namespace tls
