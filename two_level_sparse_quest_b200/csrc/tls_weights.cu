@@ -18,7 +18,7 @@
 //
 // Measured (one B200): 64 groups of 4096 listed tokens, 4 heads, bf16 13.8 us
 // (5.1 TB/s), every token of 98304 268 us (6.2 TB/s); the latent's 64 heads over
-// 4 x 2048 tokens 8.1 us, most of it the 73 KB of queries that each SM fetches.
+// 4 x 2048 tokens 7.1 us, most of it the 73 KB of queries that each SM fetches.
 //
 // The exponent is formed as tau s - lse in natural units, rounded once, before
 // it is scaled for exp2: the weights that matter have it near zero.  Each
@@ -265,7 +265,8 @@ __global__ void __launch_bounds__(kWThreads) weights_f32_kernel(WeightsArgs a) {
 
 // Threads of a CTA and CTAs of a group: as many as run at once (per_sm of 256
 // threads), no more than there are tiles; half-size CTAs where whole ones would
-// leave SMs without a tile.
+// leave SMs without a tile (quarters pay for their queries: latent 7.1 us
+// against 8.0).
 struct Split {
   int threads, ctas;
 };
@@ -275,7 +276,7 @@ Split split_of(const WeightsArgs &a, int tokens_per_warp, int per_sm) {
   const long long sms = a.num_sms > 0 ? a.num_sms : 148;
   const long long tiles = (n + tokens_per_warp - 1) / tokens_per_warp;
   int warps = kWThreads / 32;
-  while (warps > 2 && groups * ((tiles + warps - 1) / warps) < sms) warps /= 2;
+  while (warps > 4 && groups * ((tiles + warps - 1) / warps) < sms) warps /= 2;
   const long long fill = std::max<long long>(1, sms * per_sm / groups);
   return {warps * 32, static_cast<int>(std::max<long long>(1, std::min((tiles + warps - 1) / warps, fill)))};
 }
