@@ -505,3 +505,12 @@ def test_summary_of_special_values(T):
             T.tls_kv4_append(s, rows, rows, i32([t]), i32([e]), e - t, cache, label, *got)
         for g, w in zip(got, want):
             assert torch.equal(g.view(torch.int16), w.view(torch.int16)), step
+
+
+@pytest.mark.parametrize("d,G,out", [(64, 1, 0), (64, 1, 1), (64, 2, 0), (128, 1, 1)])
+def test_attention_few_outputs_shared_by_a_cluster(T, d, G, out):
+    """One or two heads over a list that takes a cluster of eight: a CTA's share of the joined outputs is less than a
+    warp, so some lanes only of one warp write between the cluster's barriers."""
+    rng = np.random.default_rng(d + G)
+    check_attention(T, 1, 2, G, d, 2500, lists(rng, 1, 2, 2500, 2300, pad=100), "list", out_dtype=out)
+    check_attention(T, 1, 1, G, d, 2500, [2500], "dense", out_dtype=out)

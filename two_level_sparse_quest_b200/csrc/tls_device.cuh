@@ -224,14 +224,21 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   return r;
 }
 // Split cluster barrier: every thread of every CTA of the cluster arrives once
-// and waits once.
+// and waits once.  The .aligned forms need the whole warp at the instruction
+// together, so each converges it first: a call may follow loops and branches
+// that only some of a warp's lanes took.
 __device__ __forceinline__ void cluster_arrive_relaxed() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_arrive_release() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 // Shared-memory address of the same variable in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t cluster_map(uint32_t local_smem_addr, uint32_t rank) {
   uint32_t a;
