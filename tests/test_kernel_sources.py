@@ -22,3 +22,25 @@ def test_aligned_cluster_barriers_converge_the_warp_first():
             seen += 1
             assert re.search(r"__syncwarp\(\);\s*$", text[:m.start()]), (name, text[max(0, m.start() - 80):m.end()])
     assert seen >= 3
+
+
+def block_after(text, head):
+    """The braced block that follows the first `head`."""
+    i = text.index("{", text.index(head) + len(head))
+    depth = 0
+    for j in range(i, len(text)):
+        depth += (text[j] == "{") - (text[j] == "}")
+        if depth == 0:
+            return text[i:j + 1]
+    raise AssertionError(head)
+
+
+def test_matrix_instructions_follow_a_converged_warp():
+    """mma.sync and movmatrix take whole warps.  Before them lie a branch that the lanes of one head take alone (the
+    attention's new maximum) and the early returns of a list's ids (the accumulated weights)."""
+    text = dict(sources())
+    moved = block_after(text["tls_kv4_attn.cu"], "__any_sync(0xffffffffu, top > kPShift + 1.f))")
+    assert "if (mx > m[nt][e])" in moved and re.search(r"__syncwarp\(\);\s*}$", moved)
+    loop = block_after(text["tls_weights.cu"], "for (; tile < tiles; tile += step)")
+    ids, first = loop.index("n1 = token_at("), min(loop.index("mma_full("), loop.index("mma_f16("))
+    assert "__syncwarp();" in loop[ids:first]

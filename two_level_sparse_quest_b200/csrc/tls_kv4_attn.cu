@@ -412,6 +412,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
                 t[nt][e + 2] = fmaf(s[nt][e + 2], sl[nt][e], kPShift - mx);
               }
             }
+          __syncwarp();  // a head's lanes branch alone; movmatrix and mma take the whole warp
         }
         // ---- O^T += V^T P^T
         uint32_t ph[NT][2], pl[NT][2];

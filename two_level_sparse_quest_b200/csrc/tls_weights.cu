@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(kWThreads, NT == 1 && D <= 128 ? 5 : 1) weight
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
     const int n0 = token_at(a, group, (tile + step) * 16 + g, n), n1 = token_at(a, group, (tile + step) * 16 + 8 + g, n);
+    __syncwarp();  // the ids' early returns branch lane by lane; mma takes the whole warp
     if constexpr (KIND == 1) {
       constexpr int NL = D / 32;              // 16-byte reads per row and lane
       constexpr int U = NL < 6 ? NL : 6;      // pairs of reads in flight
