@@ -44,3 +44,11 @@ def test_matrix_instructions_follow_a_converged_warp():
     loop = block_after(text["tls_weights.cu"], "for (; tile < tiles; tile += step)")
     ids, first = loop.index("n1 = token_at("), min(loop.index("mma_full("), loop.index("mma_f16("))
     assert "__syncwarp();" in loop[ids:first]
+
+
+def test_a_copy_that_was_given_up_on_is_waited_for_again():
+    """The attention's wait for a bulk copy has a limit.  Past it the kernel still waits, with the same limit, for the
+    copy in flight before the ring is used for something else and the CTA's shared memory goes to another one."""
+    text = dict(sources())["tls_kv4_attn.cu"]
+    gave_up = block_after(text, "if (!__all_sync(0xffffffffu, arrived))")
+    assert "atomicOr(a.err, kErrAttnWait)" in gave_up and "mbarrier_wait(&s_full[warp][st], phase)" in gave_up

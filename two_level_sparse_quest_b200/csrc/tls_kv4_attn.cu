@@ -314,11 +314,13 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
     }
     const uint32_t vm = valid[0];
     if constexpr (kBulk) {
-      if (vm != 0u) {  // a wait that gives up (which a correct run never sees): no further copies, the result is undefined
+      if (vm != 0u) {  // a wait that gives up (which a correct run never sees): no further copies, those in flight are
+                       // waited for, the result is undefined
         const bool arrived = mbarrier_wait(&s_full[warp][st], phase);
         if (!__all_sync(0xffffffffu, arrived)) {
           alive = false;
           if (lane == 0 && a.err) atomicOr(a.err, kErrAttnWait);
+          (void)mbarrier_wait(&s_full[warp][st], phase);  // its bytes may still land: not while the ring holds partials
         }
       }
     }
