@@ -390,7 +390,9 @@ TLS_API tls_status tls_kv4_read(const tls_shape *s, const void *cache, const int
  *              [B][H_kv][n_slots][bs] records, and token t of a group is record
  *              t % bs of slot slot_of_block[b][g][t / bs] (-1: skipped).  With
  *              token_idx only; n_slots * bs within int32
- *   out, lse_out  as in tls_sparse_attn_decode (no token: out 0, lse -inf)
+ *   out, lse_out  as in tls_sparse_attn_decode (no token: out 0, lse -inf).  The
+ *              softmax weights are held in 22 bits whatever out's type: a bf16
+ *              out is the fp32 out rounded once
  *   ws, ws_bytes  tls_kv4_workspace_size(s) bytes, 256-byte aligned; calls that
  *              run concurrently need separate ones */
 TLS_API tls_status tls_kv4_attn_decode(const tls_shape *s, const void *q, const void *cache,

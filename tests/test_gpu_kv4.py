@@ -514,3 +514,37 @@ def test_attention_few_outputs_shared_by_a_cluster(T, d, G, out):
     rng = np.random.default_rng(d + G)
     check_attention(T, 1, 2, G, d, 2500, lists(rng, 1, 2, 2500, 2300, pad=100), "list", out_dtype=out)
     check_attention(T, 1, 1, G, d, 2500, [2500], "dense", out_dtype=out)
+
+
+def both_outputs(T, B, H, G, d, ctx, kw, kt=64, bs=32, cache=None, seed=0):
+    """The same call with an fp32 and with a bf16 output."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    q = torch.randn((B, H * G, d), generator=g, device="cuda").to(BF16)
+    res = []
+    for out in (0, 1):
+        s = shape(T, B, H, G, d, ctx, bs=bs, kt=kt, out=out)
+        o = torch.zeros((B, H * G, d), dtype=BF16 if out else torch.float32, device="cuda")
+        lse = torch.zeros((B, H * G), device="cuda")
+        ws = torch.empty(T.tls_kv4_workspace_size(s), dtype=torch.uint8, device="cuda")
+        T.tls_kv4_attn_decode(s, q, cache, o, lse, ws=ws, **kw)
+        res.append((o, lse))
+    return res
+
+
+@pytest.mark.parametrize("d,G", [(64, 1), (64, 16), (128, 4), (128, 8), (128, 16), (128, 64)])
+@pytest.mark.parametrize("mode", ["list", "paged", "dense"])
+def test_attention_output_type_rounds_the_result_only(T, mode, d, G):
+    """A bf16 output is the fp32 output rounded once: the softmax weights carry the same bits for both."""
+    rng = np.random.default_rng(G)
+    B, H, ctx, bs, kt = 2, 2, 3000, 16, 1500
+    rec = torch.from_numpy(R.records(rng.standard_normal((B, H, ctx, d)), rng.standard_normal((B, H, ctx, d)))).cuda()
+    kw = dict(seq_lens=i32([ctx, 777]))
+    if mode != "dense":
+        kw = dict(token_idx=i32(lists(rng, B, H, ctx, kt, pad=3)))
+    if mode == "paged":
+        nb = -(-ctx // bs)
+        rec = torch.cat((rec, rec[:, :, :nb * bs - ctx]), 2).contiguous()
+        kw.update(slot_of_block=torch.arange(nb, dtype=torch.int32, device="cuda").expand(B, H, nb).contiguous(), n_slots=nb)
+    (o32, l32), (o16, l16) = both_outputs(T, B, H, G, d, ctx, kw, kt=kt, bs=bs, cache=rec)
+    assert torch.equal(l32, l16) and o32.isfinite().all() and o32.any()
+    assert torch.equal(o32.to(BF16), o16)

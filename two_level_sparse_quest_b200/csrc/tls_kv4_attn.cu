@@ -9,8 +9,8 @@
 // is the floor; at that rate an SM has 6.4 cycles for a token, and it is the
 // instructions that widen the codes (two for each pair of channels: e2m1 ->
 // fp16, times the scale, each at half rate) that come near it, not the tensor
-// pipe.  Measured (one B200): 64 groups of 98304 tokens, 4 heads, 168 us (5.4
-// TB/s, 0.82 of the measured copy rate); of 4096 listed ones 19.7 us.
+// pipe.  Measured (one B200): 64 groups of 98304 tokens, 4 heads, 174 us (5.2
+// TB/s, 0.80 of the measured copy rate); of 4096 listed ones 19.2 us.
 //
 // Layout: the tokens are the MMA rows.  S^T[16 tokens x 8 heads] = K q^T takes
 // one m16n8k16 per 16 channels, O^T[16 channels x 8 heads] += V^T P^T one per
@@ -24,13 +24,16 @@
 // codes, a nibble of each token in a byte, before they are widened.
 //
 // Numerics: K and V are exact in fp16; q is (tls_kv4.cuh, q_norm); sums are
-// fp32.  P is 2^(s - m + 14), at most 2^15, in fp16 (what falls below 2^-38 of
-// the largest weight is dropped); m is a running reference that moves only
-// when a score exceeds it by more than one (log2).  For an fp32 output P is
-// two fp16 parts, high and low (22 bits): with one it would be off by 1e-4.
-// A bf16 output takes one part, whose 2^-12 per weight is an eighth of the
-// output's own rounding and averages out over the tokens; the sum l is of the
-// unrounded weights in both.
+// fp32.  P is 2^(s - m + 14), at most 2^15, as two fp16 parts, high and low
+// (22 bits; what falls below 2^-38 of the largest weight is dropped), whatever
+// the output's type, and the sum l is of the unrounded weights: with the high
+// part alone each weight would be off by up to 2^-11, which moves a bf16
+// output by a step now and then.  m is a running reference that moves only
+// when a score exceeds it by more than one (log2).  A unit of at most four
+// heads leaves four of the eight columns free: they repeat the heads' queries
+// and carry the low parts, so that P's second part costs no MMA (every token
+// of 8 x 96k, 4 heads: 174 us against 192 with two MMAs; 8 heads 200 with two,
+// 177 with the high part alone).
 //
 // Work split: a unit is one group (or 16 of its heads).  A thread-block
 // cluster of up to 8 CTAs takes a unit, every warp 32-token tiles in turn
@@ -107,7 +110,7 @@ __device__ __forceinline__ float2 ld_cluster(uint32_t addr) {
 // (rows 2c) collide in shared memory at d 128.
 __device__ __forceinline__ int row_token(int row) { return (0x57463120u >> (4 * row)) & 15; }
 
-template <int D, int NT, bool LIST, bool PAGED, bool F32OUT>
+template <int D, int NT, bool LOCOL, bool LIST, bool PAGED>
 __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(Kv4AttnArgs a) {
   using R = Kv4Rec<D>;
   using L = Kv4Smem<D, NT>;
@@ -172,13 +175,14 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
   // some are missing, eight lanes bring a record's first eight chunks and every
   // lane its own record's ninth, zero-filled.  (One bulk copy per listed record
   // was slower: 24.0 us against 20.4 for 8 x 96k, 4096 tokens.)
-  // The queries' loads go out first (warps below NT, one block of 8 heads each).
+  // The queries' loads go out first (warps below NT, one block of 8 columns each).
   uint4 qv[D / 32];
   if (warp < NT) {
+    const int h = LOCOL ? g & 3 : warp * 8 + g;  // LOCOL: columns 4 .. 7 repeat the heads of 0 .. 3
     const uint4 *qp = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) +
-                                                      (static_cast<size_t>(b) * a.n_q_heads + head0 + warp * 8 + g) * D + c * (D / 4));
+                                                      (static_cast<size_t>(b) * a.n_q_heads + head0 + h) * D + c * (D / 4));
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) qv[i] = warp * 8 + g < HG ? qp[i] : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < D / 32; ++i) qv[i] = h < HG ? qp[i] : make_uint4(0u, 0u, 0u, 0u);
   }
   uint32_t valid[kRing];  // valid tokens of the stages in flight, oldest first
 #pragma unroll
@@ -429,11 +433,14 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             const __half2 hi = __floats2half2_rn(p[2 * r], p[2 * r + 1]);
-            ph[nt][r] = movmatrix(*reinterpret_cast<const uint32_t *>(&hi));
-            if constexpr (F32OUT) {
-              const float2 hf2 = __half22float2(hi);
-              const __half2 lo = __floats2half2_rn(p[2 * r] - hf2.x, p[2 * r + 1] - hf2.y);
-              pl[nt][r] = movmatrix(*reinterpret_cast<const uint32_t *>(&lo));
+            const float2 hf2 = __half22float2(hi);
+            const __half2 lo = __floats2half2_rn(p[2 * r] - hf2.x, p[2 * r + 1] - hf2.y);
+            const uint32_t uh = *reinterpret_cast<const uint32_t *>(&hi), ul = *reinterpret_cast<const uint32_t *>(&lo);
+            if constexpr (LOCOL) {
+              ph[nt][r] = movmatrix(c < 2 ? uh : ul);
+            } else {
+              ph[nt][r] = movmatrix(uh);
+              pl[nt][r] = movmatrix(ul);
             }
           }
         }
@@ -470,7 +477,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               mma_f16(o[nt][4 * q + j], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
-              if constexpr (F32OUT) mma_f16(o[nt][4 * q + j], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+              if constexpr (!LOCOL) mma_f16(o[nt][4 * q + j], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
             }
           }
         }
@@ -485,6 +492,12 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
   if constexpr (!kBulk) cp_async_wait<0>();
   __syncwarp();
 
+  if constexpr (LOCOL) {  // a head's sum over the high parts (lane c) and over the low parts (lane c + 2)
+#pragma unroll
+    for (int j = 0; j < OT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[0][j][e] += __shfl_xor_sync(0xffffffffu, o[0][j][e], 2);
+  }
   // ---- the warp's partial into its own ring
   float *po = reinterpret_cast<float *>(ring);
 #pragma unroll
@@ -705,10 +718,10 @@ void kv4_plan(Kv4AttnArgs &a, int n_max) {
     }
 }
 
-template <int D, int NT, bool LIST, bool PAGED, bool F32OUT>
+template <int D, int NT, bool LOCOL, bool LIST, bool PAGED>
 cudaError_t run(const Kv4AttnArgs &a, cudaStream_t st) {
   using L = Kv4Smem<D, NT>;
-  auto kern = kv4_attn_kernel<D, NT, LIST, PAGED, F32OUT>;
+  auto kern = kv4_attn_kernel<D, NT, LOCOL, LIST, PAGED>;
   static bool configured[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -721,14 +734,15 @@ cudaError_t run(const Kv4AttnArgs &a, cudaStream_t st) {
   return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(ctas)), dim3(kWarps * 32), L::kSmem, st, a.cluster, a);
 }
 
-template <int D, int NT, bool F32OUT>
+template <int D, int NT, bool LOCOL>
 cudaError_t dispatch(const Kv4AttnArgs &a, cudaStream_t st) {
-  if (!a.token_idx) return run<D, NT, false, false, F32OUT>(a, st);
-  return a.slot_of_block ? run<D, NT, true, true, F32OUT>(a, st) : run<D, NT, true, false, F32OUT>(a, st);
+  if (!a.token_idx) return run<D, NT, LOCOL, false, false>(a, st);
+  return a.slot_of_block ? run<D, NT, LOCOL, true, true>(a, st) : run<D, NT, LOCOL, true, false>(a, st);
 }
-template <int D, int NT>
+template <int D>
 cudaError_t dispatch(const Kv4AttnArgs &a, cudaStream_t st) {
-  return a.out_dtype == 1 ? dispatch<D, NT, false>(a, st) : dispatch<D, NT, true>(a, st);
+  if (a.head_chunk <= 4) return dispatch<D, 1, true>(a, st);
+  return a.head_chunk <= 8 ? dispatch<D, 1, false>(a, st) : dispatch<D, 2, false>(a, st);
 }
 
 }  // namespace
@@ -739,9 +753,7 @@ size_t kv4_attn_part_floats(int heads_per_group, int d, int num_sms) {
 
 cudaError_t launch_kv4_attention(Kv4AttnArgs a, cudaStream_t st) {
   kv4_plan(a, a.token_idx ? a.k_t : a.max_ctx);
-  cudaError_t e;
-  if (a.d == 128) e = a.head_chunk > 8 ? dispatch<128, 2>(a, st) : dispatch<128, 1>(a, st);
-  else e = a.head_chunk > 8 ? dispatch<64, 2>(a, st) : dispatch<64, 1>(a, st);
+  const cudaError_t e = a.d == 128 ? dispatch<128>(a, st) : dispatch<64>(a, st);
   if (e != cudaSuccess || a.n_split == 1) return e;
   const dim3 grid(a.batch * a.n_q_heads);  // units times their heads
   if (a.d == 128) return launch_pdl(kv4_merge_kernel<128>, grid, dim3(kMergeGroups * 128), 0, st, a);
