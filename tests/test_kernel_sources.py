@@ -37,13 +37,14 @@ def block_after(text, head):
 
 def test_matrix_instructions_follow_a_converged_warp():
     """mma.sync and movmatrix take whole warps.  Before them lie a branch that the lanes of one head take alone (the
-    attention's new maximum) and the early returns of a list's ids (the accumulated weights)."""
+    attention's new maximum), and the ids and the adds of a tile (the accumulated weights)."""
     text = dict(sources())
     moved = block_after(text["tls_kv4_attn.cu"], "__any_sync(0xffffffffu, top > kPShift + 1.f))")
     assert "if (mx > m[nt][e])" in moved and re.search(r"__syncwarp\(\);\s*}$", moved)
-    loop = block_after(text["tls_weights.cu"], "for (; tile < tiles; tile += step)")
-    ids, first = loop.index("n1 = token_at("), min(loop.index("mma_full("), loop.index("mma_f16("))
-    assert "__syncwarp();" in loop[ids:first]
+    weights = text["tls_weights.cu"]
+    for head in ("int token_at(const WeightsArgs &a, int group, int j, int n)", "void add_weight(float *p, float v, bool on)",
+                 "for (; tile < tiles; tile += step)"):  # no branch of single lanes at all
+        assert not re.search(r"\bif\s*\(", block_after(weights, head)), head
 
 
 def test_a_copy_that_was_given_up_on_is_waited_for_again():

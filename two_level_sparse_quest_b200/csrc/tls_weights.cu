@@ -40,15 +40,19 @@ constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ int n_tokens(const WeightsArgs &a, int b) {
   return a.token_idx ? a.k_t : min(max(a.seq_lens[b], 0), a.max_ctx);
 }
-// Token at position j of the group's list (or the j-th token), -1 if none.
+// Token at position j of the group's list (or the j-th token), -1 if none; n > 0.
+// Without a branch of single lanes, so that a warp stays together for its matrix
+// instructions.
 __device__ __forceinline__ int token_at(const WeightsArgs &a, int group, int j, int n) {
-  if (j >= n) return -1;
-  if (!a.token_idx) return j;
-  const int t = a.token_idx[static_cast<size_t>(group) * a.k_t + j];
-  return (t >= 0 && t < a.max_ctx) ? t : -1;
+  const int at = min(j, n - 1);
+  const int t = a.token_idx ? a.token_idx[static_cast<size_t>(group) * a.k_t + at] : at;
+  return (j < n && t >= 0 && t < a.max_ctx) ? t : -1;
 }
-__device__ __forceinline__ void add_weight(float *p, float v) {
-  asm volatile("red.global.add.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory");
+// *p += v where on: predicated, for the same reason.
+__device__ __forceinline__ void add_weight(float *p, float v, bool on) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n @p red.global.add.f32 [%0], %1;\n}\n" ::"l"(p), "f"(v),
+               "r"(static_cast<uint32_t>(on))
+               : "memory");
 }
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 // exp(x) for the sum; a head whose attention saw no token (lse = -inf) gives 0.
@@ -139,7 +143,6 @@ __global__ void __launch_bounds__(kWThreads, NT == 1 && D <= 128 ? 5 : 1) weight
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
     const int n0 = token_at(a, group, (tile + step) * 16 + g, n), n1 = token_at(a, group, (tile + step) * 16 + 8 + g, n);
-    __syncwarp();  // the ids' early returns branch lane by lane; mma takes the whole warp
     if constexpr (KIND == 1) {
       constexpr int NL = D / 32;              // 16-byte reads per row and lane
       constexpr int U = NL < 6 ? NL : 6;      // pairs of reads in flight
@@ -205,12 +208,11 @@ __global__ void __launch_bounds__(kWThreads, NT == 1 && D <= 128 ? 5 : 1) weight
         w0 += weight_of(s[nt][e], p.x, p.y);
         w1 += weight_of(s[nt][e + 2], p.x, p.y);
       }
-    w0 += __shfl_xor_sync(0xffffffffu, w0, 1);
-    w1 += __shfl_xor_sync(0xffffffffu, w1, 1);
-    w0 += __shfl_xor_sync(0xffffffffu, w0, 2);
-    w1 += __shfl_xor_sync(0xffffffffu, w1, 2);
-    if (c == 0 && t0 >= 0) add_weight(out + t0, w0);
-    if (c == 1 && t1 >= 0) add_weight(out + t1, w1);
+    float v = c & 1 ? w1 : w0;  // even lanes sum row g's token, odd ones row g + 8's
+    v += __shfl_xor_sync(0xffffffffu, c & 1 ? w0 : w1, 1);
+    v += __shfl_xor_sync(0xffffffffu, v, 2);
+    const int tt = c & 1 ? t1 : t0;
+    add_weight(out + tt, v, c < 2 && tt >= 0);
     t0 = n0;
     t1 = n1;
   }
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(kWThreads) weights_f32_kernel(WeightsArgs a) {
       s0 += __shfl_xor_sync(0xffffffffu, s0, 2);
       w += weight_of(s0, a.scale, lse[h]);
     }
-    if (c == 0 && t >= 0) add_weight(out + t, w);
+    add_weight(out + t, w, c == 0 && t >= 0);
   }
 }
 
