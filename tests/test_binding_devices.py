@@ -45,3 +45,29 @@ def test_stream_argument(T):
         cuda_stream = 77
 
     assert T._stream(5) == 5 and T._stream(Stream()) == 77
+
+
+def test_binding_does_without_the_private_names_of_a_cuda_build():
+    """A build of torch without torch._C._cuda_getDevice and _cuda_getCurrentRawStream (CPU builds have neither): the
+    binding is imported, and its device and stream come from torch.cuda's public calls."""
+    import os
+    import subprocess
+    import sys
+
+    code = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+from two_level_sparse_quest_b200 import tls as T
+class Stream:
+    cuda_stream = 77
+torch.cuda.is_initialized = lambda: True
+torch.cuda.current_device = lambda: 3
+torch.cuda.current_stream = lambda device=None: Stream()
+assert T._current_device() == 3 and T._raw_stream(3) == 77 and T._stream(None) == 77 and T._stream(5) == 5
+print("ok")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr

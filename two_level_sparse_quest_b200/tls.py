@@ -142,10 +142,11 @@ def _dptr(x):
     return _ptr(x)
 
 
-# The plain forms of torch.cuda.current_device() and torch.cuda.current_stream().cuda_stream: the objects that those
-# build cost a call 3 us.
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# The current device, and the handle of a device's current stream.  Where torch has them (its CUDA builds), the plain
+# functions below torch.cuda's public ones: the objects that those build cost a call 3 us.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
+_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+               or (lambda device: torch.cuda.current_stream(device).cuda_stream))
 
 
 def _dptrs(*xs):
