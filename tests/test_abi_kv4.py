@@ -196,3 +196,17 @@ def test_kept_ids_of_the_tests_by_hand():
     assert R.keep(w, 8, 5, 1, 1).tolist() == [0, 1, 2, 5, 7]  # 1.0 twice: the lower index
     assert R.keep(w, 8, 7, 0, 0).tolist() == [0, 1, 2, 3, 4, 5, 7]  # NaN goes first
     assert R.keep(w, 3, 4, 1, 1).tolist() == [0, 1, 2]
+
+
+def test_an_empty_batch_moves_nothing(T):
+    """batch 0: the arrays are empty, and an empty tensor's pointer is NULL."""
+    import torch
+
+    s = good(T, batch=0)
+    st = T._lib.tls_evict_compact(by(s), 100, None, None, 2, (ctypes.c_void_p * 2)(None, None),
+                                  (ctypes.c_int32 * 2)(256, 144), None, None)
+    assert st == T.TLS_OK, T.tls_last_error()
+    st = T._lib.tls_evict_compact(by(s), 100, None, None, 1, (ctypes.c_void_p * 1)(None), (ctypes.c_int32 * 1)(0), None, None)
+    assert st == T.TLS_ERR_INVALID_ARG and "row_bytes[0]" in T.tls_last_error()
+    assert torch.empty((0, 8, 4096, 144)).data_ptr() == 0
+    T.tls_evict_compact(s, 100, None, None, [(0, 256)], None, stream=1)

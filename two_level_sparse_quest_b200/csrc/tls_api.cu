@@ -874,12 +874,12 @@ tls_status tls_evict_compact(const tls_shape *s, int32_t budget, const int32_t *
   if (n_rows < 0 || n_rows > tls::kMaxEvictRows)
     return fail(TLS_ERR_INVALID_ARG, "n_rows %d outside [0, %d]", n_rows, tls::kMaxEvictRows);
   if (n_rows > 0 && (!rows || !row_bytes)) return fail(TLS_ERR_INVALID_ARG, "rows or row_bytes is NULL");
-  for (int i = 0; i < n_rows; ++i) {
-    if (!rows[i]) return fail(TLS_ERR_INVALID_ARG, "rows[%d] is NULL", i);
+  for (int i = 0; i < n_rows; ++i)
     if (row_bytes[i] < 1 || row_bytes[i] > 65536)
       return fail(TLS_ERR_INVALID_ARG, "row_bytes[%d] = %d outside [1, 65536]", i, row_bytes[i]);
-  }
   if (s->batch == 0 || (n_rows == 0 && !weights)) return TLS_OK;
+  for (int i = 0; i < n_rows; ++i)
+    if (!rows[i]) return fail(TLS_ERR_INVALID_ARG, "rows[%d] is NULL", i);
   CHECK_PTR(keep_idx, 4);
   CHECK_PTR(seq_lens, 4);
   if (weights) CHECK_PTR(weights, 4);
