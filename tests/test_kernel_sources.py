@@ -53,3 +53,16 @@ def test_a_copy_that_was_given_up_on_is_waited_for_again():
     text = dict(sources())["tls_kv4_attn.cu"]
     gave_up = block_after(text, "if (!__all_sync(0xffffffffu, arrived))")
     assert "atomicOr(a.err, kErrAttnWait)" in gave_up and "mbarrier_wait(&s_full[warp][st], phase)" in gave_up
+
+
+def test_every_launcher_has_a_caller():
+    """Each host launcher that a header declares is called from another file than the one that defines it."""
+    names, text = set(), dict(sources())
+    for name in sorted(os.listdir(CSRC)):
+        if name.endswith(".h"):
+            with open(os.path.join(CSRC, name)) as f:
+                names |= set(re.findall(r"cudaError_t (launch_\w+)\(", f.read()))
+    assert len(names) > 10
+    for n in sorted(names):
+        users = [f for f, t in text.items() if re.search(rf"\b{n}\(", t) and not re.search(rf"cudaError_t {n}\(", t)]
+        assert users, n

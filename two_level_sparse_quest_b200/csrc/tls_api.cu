@@ -569,7 +569,7 @@ static tls_status prefetch_diff(const tls_shape *s, int32_t n_slots, long long b
   a.n_blocks_max = n_blocks_max(s);
   a.k_b = s->k_b;
   a.n_slots = n_slots;
-  return cuda_status(tls::launch_prefetch_diff_bytes(a, static_cast<int>(block_bytes), static_cast<cudaStream_t>(stream)),
+  return cuda_status(tls::launch_prefetch_diff(a, static_cast<int>(block_bytes), static_cast<cudaStream_t>(stream)),
                      "prefetch_diff launch");
 }
 

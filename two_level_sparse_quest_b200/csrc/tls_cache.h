@@ -71,7 +71,4 @@ struct CompactArgs {
 };
 cudaError_t launch_evict_compact(const CompactArgs &a, cudaStream_t st);
 
-// launch_prefetch_diff for blocks of any size (a multiple of 16 bytes); a's d, block_size and dtype are not read.
-cudaError_t launch_prefetch_diff_bytes(const OffloadArgs &a, int block_bytes, cudaStream_t st);
-
 }  // namespace tls

@@ -187,9 +187,10 @@ struct OffloadArgs {
   const int32_t *next_block_idx;
   int32_t *n_new;
   int32_t *jobs;
-  int batch, n_kv_heads, d, block_size, n_blocks_max, k_b, n_slots, dtype;
+  int batch, n_kv_heads, n_blocks_max, k_b, n_slots;
 };
 cudaError_t launch_offload_reset(const OffloadArgs &a, cudaStream_t st);
-cudaError_t launch_prefetch_diff(const OffloadArgs &a, cudaStream_t st);
+// block_bytes: of one block in host_kv and in a slot (a multiple of 16).
+cudaError_t launch_prefetch_diff(const OffloadArgs &a, int block_bytes, cudaStream_t st);
 
 }  // namespace tls

@@ -13,7 +13,6 @@
 // over PCIe with 16-byte loads and writes it into its slot.  Both run on the
 // caller's copy stream, so the transfer overlaps the attention of the current
 // step on the compute stream.
-#include "tls_cache.h"
 #include "tls_device.cuh"
 #include "tls_internal.h"
 
@@ -143,15 +142,11 @@ cudaError_t launch_offload_reset(const OffloadArgs &a, cudaStream_t st) {
   return launch_pdl(fill_neg1_kernel, dim3(64), dim3(256), 0, st, a.block_of_slot, groups * a.n_slots);
 }
 
-cudaError_t launch_prefetch_diff_bytes(const OffloadArgs &a, int block_bytes, cudaStream_t st) {
+cudaError_t launch_prefetch_diff(const OffloadArgs &a, int block_bytes, cudaStream_t st) {
   const int groups = a.batch * a.n_kv_heads;
   cudaError_t e = launch_pdl(prefetch_diff_kernel, dim3(groups), dim3(kDiffThreads), 0, st, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(copy_blocks_kernel, dim3(a.k_b, groups), dim3(256), 0, st, a, block_bytes);
-}
-
-cudaError_t launch_prefetch_diff(const OffloadArgs &a, cudaStream_t st) {
-  return launch_prefetch_diff_bytes(a, 2 * a.block_size * a.d * (a.dtype == 1 ? 2 : 4), st);
 }
 
 }  // namespace tls
