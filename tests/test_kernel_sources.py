@@ -61,7 +61,7 @@ def test_every_launcher_has_a_caller():
     for name in sorted(os.listdir(CSRC)):
         if name.endswith(".h"):
             with open(os.path.join(CSRC, name)) as f:
-                names |= set(re.findall(r"cudaError_t (launch_\w+)\(", f.read()))
+                names |= set(re.findall(r"cudaError_t (launch_\w+)\([^;{]*\);", f.read()))  # declared, not defined
     assert len(names) > 10
     for n in sorted(names):
         seen = sum(len(re.findall(rf"\b{n}\(", t)) for t in text.values())
