@@ -430,3 +430,96 @@ def test_compact_weights_alone(T):
     want[:, :, :45] = 0
     want[0, 0, :3], want[0, 1, :4] = w0[0, 0, [1, 4, 30]], w0[0, 1, [0, 1, 2, 44]]
     assert torch.equal(w, want)
+
+
+def late_gaps(rng, B, H, lens, budget):
+    """Kept ids that are the identity for a while, then ever sparser: rows move by little, then by much."""
+    keeps = []
+    for n in lens:
+        per_head = []
+        for _ in range(H):
+            k = min(n, budget)
+            head = k // 2 if n > budget else k
+            rest = np.sort(rng.permutation(np.arange(head, n))[:k - head])
+            per_head.append(np.concatenate([np.arange(head), rest]))
+        keeps.append(per_head)
+    return keeps
+
+
+@pytest.mark.parametrize("offset,rows,ctx,budget", [(0, [256, 256], 3000, 1500), (1, [256], 1100, 500), (2, [256, 32], 1100, 500),
+                                                    (0, [144], 3000, 2900)])
+def test_compact_many_groups_over_several_chunks(T, offset, rows, ctx, budget):
+    """64 groups and more: each slice is moved by one large CTA, chunk after chunk, a chunk's stores directly before
+    the next one's loads (256 rows a chunk with 16-byte accesses, 16 with single bytes)."""
+    rng = np.random.default_rng(offset + len(rows))
+    B, H = (8, 8) if len(rows) > 1 else (16, 8)
+    lens = [ctx, ctx - 1, ctx // 2, budget, budget + 1, 1, 0, ctx] * (B // 8)
+    for keeps in (late_gaps(rng, B, H, lens, budget), random_keeps(rng, B, H, lens, budget)):
+        run_compact(T, B, H, ctx, lens, budget, keeps, rows, offset=offset)
+
+
+def test_stored_values_and_summary_over_evictions(T):
+    """Prompt, eviction, rebuilt summary, appended tokens, again and again: every live row holds exactly the values of
+    its token (only the sign of a zero may differ), the rebuilt summary is the max / min of the stored keys, and
+    appended rows enter it as given."""
+    rng = np.random.default_rng(11)
+    B, H, d, ctx, bs, budget = 2, 3, 128, 260, 32, 130
+    s = make(T, B, H, 1, d, ctx, bs=bs)
+    nb = -(-ctx // bs)
+    dev = dict(device="cuda")
+    cache = torch.zeros((B, H, ctx, 9 * d // 8), dtype=torch.uint8, **dev)
+    meta, label = torch.zeros((B, H, nb, 2, d), dtype=BF16, **dev), i32(list(range(16)))
+    w = torch.zeros((B, H, ctx), **dev)
+    keep, tmp = torch.zeros((B, H, budget), dtype=torch.int32, **dev), torch.zeros((B,), dtype=torch.int32, **dev)
+    lens = [0, 0]
+    K_at, V_at = np.zeros((B, H, ctx, d)), np.zeros((B, H, ctx, d))  # the values stored at each row
+    K_sum = np.zeros((B, H, ctx, d))  # the keys that the summary knows: as given, or as stored since the last rebuild
+
+    def check():
+        torch.cuda.synchronize()
+        got = cache.cpu().numpy()
+        m = f64(meta)
+        for b in range(B):
+            n = lens[b]
+            gk, gv = R.split(got[b, :, :n], d)
+            np.testing.assert_array_equal(gk, K_at[b, :, :n])
+            np.testing.assert_array_equal(gv, V_at[b, :, :n])
+            for blk in range(-(-n // bs)):
+                part = K_sum[b, :, blk * bs:min(n, (blk + 1) * bs)]
+                np.testing.assert_array_equal(m[b, :, blk, 0], part.max(1))
+                np.testing.assert_array_equal(m[b, :, blk, 1], part.min(1))
+
+    def append(counts):
+        n = max(counts)
+        rows = [torch.from_numpy(rng.standard_normal((B, H, n, d)).astype(np.float32)).to(BF16) for _ in range(2)]
+        old, new = i32(lens), i32([a + c for a, c in zip(lens, counts)])
+        T.tls_kv4_append(s, rows[0].cuda(), rows[1].cuda(), old, new, n, cache, label, meta, None)
+        K, V = (R.value(*R.quantise(f64(x))) for x in rows)
+        for b in range(B):
+            K_at[b, :, lens[b]:lens[b] + counts[b]], V_at[b, :, lens[b]:lens[b] + counts[b]] = K[b, :, :counts[b]], V[b, :, :counts[b]]
+            K_sum[b, :, lens[b]:lens[b] + counts[b]] = f64(rows[0])[b, :, :counts[b]]
+            lens[b] += counts[b]
+
+    append([250, 131])
+    check()
+    for turn in range(3):
+        w.copy_(torch.from_numpy(heavy(rng, (B, H, ctx))))
+        T.tls_evict_select(s, budget, 4, 20, w, i32(lens), keep, tmp)
+        T.tls_evict_compact(s, budget, keep, i32(lens), [cache], w)
+        ids = keep.cpu().numpy()
+        for b in range(B):
+            for h in range(H):
+                k = ids[b, h][ids[b, h] >= 0]
+                assert len(k) == min(lens[b], budget)
+                K_at[b, h, :len(k)], V_at[b, h, :len(k)] = K_at[b, h, k], V_at[b, h, k]
+            lens[b] = min(lens[b], budget)
+        K = torch.zeros((B, H, ctx, d), dtype=BF16, **dev)
+        T.tls_kv4_read(s, cache, torch.zeros_like(tmp), tmp, ctx, K)
+        T.tls_build_block_meta(s, K, tmp, label, meta, None)
+        K_sum[:] = K_at
+        check()
+        append([1, 1])
+        check()
+        append([100 - turn, 37])
+        check()
+    assert T.tls_device_error(clear=True) == 0

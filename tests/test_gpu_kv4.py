@@ -548,3 +548,53 @@ def test_attention_output_type_rounds_the_result_only(T, mode, d, G):
     (o32, l32), (o16, l16) = both_outputs(T, B, H, G, d, ctx, kw, kt=kt, bs=bs, cache=rec)
     assert torch.equal(l32, l16) and o32.isfinite().all() and o32.any()
     assert torch.equal(o32.to(BF16), o16)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [1, 4, 8, 16, 32, 64])
+def test_attention_heads_over_long_lists_and_slots(T, d, G):
+    """Lists of a few thousand tokens (clusters or parts), bf16 output, over the cache and over a slot cache of which
+    some blocks are missing."""
+    rng = np.random.default_rng(d + G)
+    ctx, kt = 4100, 3001
+    H = 2 if G < 16 else 1
+    check_attention(T, 1, H, G, d, ctx, lists(rng, 1, H, ctx, kt, pad=7), "list", out_dtype=1)
+    check_attention(T, 1, H, G, d, ctx, lists(rng, 1, H, ctx, kt, pad=7), "paged", bs=16, slots=200, out_dtype=G > 4)
+    check_attention(T, 2, H, G, d, 400, lists(rng, 2, H, 400, 131), "paged", bs=32, out_dtype=G <= 4)
+
+
+@pytest.mark.parametrize("d,G,out", [(64, 64, 0), (128, 32, 0), (128, 64, 1), (64, 32, 1), (128, 16, 0)])
+def test_attention_many_heads_over_a_long_cache(T, d, G, out):
+    """Every token of 20001, in several units of 16 heads and many parts; a short sequence beside it."""
+    check_attention(T, 2, 1, G, d, 20001, [20001, 33], "dense", out_dtype=out)
+
+
+def test_attention_calls_at_once(T):
+    """Calls on several streams at the same time, each with its own workspace and output, give the bits of calls one
+    after another."""
+    rng = np.random.default_rng(3)
+    B, H, G, d, ctx = 1, 2, 4, 128, 20000
+    rec = torch.from_numpy(R.records(rng.standard_normal((B, H, ctx, d)), rng.standard_normal((B, H, ctx, d)))).cuda()
+    s = shape(T, B, H, G, d, ctx, kt=2000)
+    tok, lens = i32(lists(rng, B, H, ctx, 2000)), i32([ctx])
+    n = 4
+    q = [bf16_rows(rng, (B, H * G, d), 1.0, False).cuda() for _ in range(n)]
+    ws = [torch.empty(T.tls_kv4_workspace_size(s), dtype=torch.uint8, device="cuda") for _ in range(n)]
+
+    def run(i, out, w, stream=None):
+        kw = dict(token_idx=tok) if i % 2 else dict(seq_lens=lens)
+        T.tls_kv4_attn_decode(s, q[i], rec, out, ws=ws[i], stream=stream, **kw)
+        T.tls_kv4_accum_weights(s, q[i], rec, torch.zeros((B, H * G), device="cuda"), w, stream=stream, **kw)
+
+    outs = [[torch.zeros((B, H * G, d), device="cuda") for _ in range(n)] for _ in range(2)]
+    sums = [[torch.zeros((B, H, ctx), device="cuda") for _ in range(n)] for _ in range(2)]
+    for i in range(n):
+        run(i, outs[0][i], sums[0][i])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(n)]
+    for i in range(n):
+        with torch.cuda.stream(streams[i]):
+            run(i, outs[1][i], sums[1][i])
+    torch.cuda.synchronize()
+    for i in range(n):
+        assert torch.equal(outs[0][i], outs[1][i]) and torch.equal(sums[0][i], sums[1][i])
