@@ -410,8 +410,13 @@ cudaError_t launch_evict_compact(const CompactArgs &a, cudaStream_t st) {
   }
   p.first[a.n_rows] = slices;
   // Slices that nearly fill the SMs by themselves take a large CTA each: its
-  // barrier is cheaper than a cluster's (64 groups 568 us against 613, 48
-  // groups 462 against 547; with 32 groups, 96 slices, 390 against 356).
+  // barrier is cheaper than a cluster's.  Half of 32768 tokens a group, large
+  // CTAs against clusters: K, V in bf16 and weights 32 groups (96 slices) 126 us
+  // against 114, 40 (120) 136 against 166, 64 184 against 197; 4-bit records and
+  // weights 48 groups (96) 77 against 62, 64 (128) 83 against 98.  Over 65 such
+  // counts (six row layouts, 4 to 256 groups) the rule is within 1 % of the
+  // better of the two on average; it is furthest off where the slices are one and
+  // a bit or nearly two waves (96 groups of d 64 rows 158 against 145).
   const long long units = static_cast<long long>(groups) * slices;
   if (units * 5 >= 4LL * sms) {
     p.cluster = 1;
