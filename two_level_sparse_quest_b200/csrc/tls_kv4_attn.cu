@@ -679,19 +679,20 @@ int max_parts(int sms) { return 4 * sms; }
 // How a call is cut: heads per unit, and either CTAs per cluster or parts per
 // unit (joined by a second launch), whichever this estimate in tenths of a
 // microsecond finds cheapest.  A warp takes 1.9 us for a tile when two CTAs
-// share an SM and 1.1 us alone (16 heads, always alone: 1.6 us); a wave of CTAs
-// costs 3.5 us around its tiles, a cluster 1 us, the second launch 3.  It is a
-// rule to choose by and no prediction: fitted at d 128, 4 heads, it counts a
-// wave that is hardly begun as a whole one and so misjudges cuts that it does
-// not take.  Measured over 680 shapes (both d; 4, 8 and 16 heads; 1 to 256
-// units; lists of 128 to 8192 tokens and every one of up to 98304) its choice
-// is within 1.1 % of the best cut on average and within 5 % for 94 of 100; the
-// worst is 16 units of 8192 listed tokens (16.7 us with clusters of 8, 13.2 as
-// 18 parts).  Some of them: 64 units of 4096 listed tokens 19.6 us with
-// clusters of 4 (one wave), 22.5 with 2, 22.9 as 4 parts, 24.7 with 8, 25.7 as
-// 9 parts; 64 units of 98304 tokens 173 us as 9 parts (two full waves), 189 with
-// clusters of 4, 200 with 8; 96 units of 32768 tokens, 16 heads, 175 us as 3
-// parts, 222 whole.
+// share an SM and 1.1 us alone, a wave of CTAs costs 3.5 us around its tiles;
+// 16 heads, always alone on their SM, 1.7 us and 15 us (nothing covers a wave's
+// start and its joins); a cluster 1 us, the second launch 3.  It is a rule to
+// choose by and no prediction: fitted at d 128, it counts a wave that is hardly
+// begun as a whole one and so misjudges cuts that it does not take.  Measured
+// over 680 shapes (both d; 4, 8 and 16 heads; 1 to 256 units; lists of 128 to
+// 8192 tokens and every one of up to 98304) its choice is within 1.1 % of the
+// best cut on average and within 5 % for 94 of 100; the worst is 16 units of
+// 8192 listed tokens (16.7 us with clusters of 8, 13.2 as 18 parts).  Some of
+// them: 64 units of 4096 listed tokens 19.6 us with clusters of 4 (one wave),
+// 22.5 with 2, 22.9 as 4 parts, 24.7 with 8, 25.7 as 9 parts; 64 units of 98304
+// tokens 173 us as 9 parts (two full waves), 189 with clusters of 4, 200 with 8;
+// with 16 heads 338 with clusters of 2, 348 as 9 parts, and 96 units of 32768
+// tokens 187 us as 3 parts, 229 whole.
 void kv4_plan(Kv4AttnArgs &a, int n_max) {
   const int G = a.n_q_heads / a.n_kv_heads;
   a.head_chunk = std::min(G, 16);
@@ -710,8 +711,8 @@ void kv4_plan(Kv4AttnArgs &a, int n_max) {
     const long long ctas = static_cast<long long>(units) * per_unit;
     const int rounds = (tiles + per_unit * kWarps - 1) / (per_unit * kWarps);
     const long long waves = (ctas + places(cluster) - 1) / places(cluster);
-    const int tile = resident == sms ? 16 : ctas <= sms ? 11 : 19;  // one CTA an SM, for 16 heads or for lack of CTAs; or two
-    const long long cost = waves * (35 + rounds * tile) + (cluster > 1 ? 10 : 0) + (n_split > 1 ? 30 : 0);
+    const int wave = resident == sms ? 150 : 35, tile = resident == sms ? 17 : ctas <= sms ? 11 : 19;
+    const long long cost = waves * (wave + rounds * tile) + (cluster > 1 ? 10 : 0) + (n_split > 1 ? 30 : 0);
     if (best < 0 || cost < best) {
       best = cost;
       a.cluster = cluster;
