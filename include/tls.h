@@ -366,8 +366,9 @@ TLS_API size_t tls_kv4_workspace_size(const tls_shape *s);
  *   row_stride  rows per (sequence, KV head) in K and V, at most max_ctx (0: no-op)
  *   meta        the block summary of tls_build_block_meta, right for the tokens
  *               below old_lens, or NULL; afterwards it holds the bits that
- *               tls_build_block_meta gives for all given rows (the rows as
- *               given, not as stored)
+ *               tls_build_block_meta gives for all given rows: the rows as
+ *               given, not as stored, so that a stored key, which is rounded,
+ *               may pass its block's max or min by half a step of its code
  *   slab, label_idx  the label slab and its channels, or NULL; an int8 slab
  *               returns TLS_ERR_UNSUPPORTED (rebuild it) */
 TLS_API tls_status tls_kv4_append(const tls_shape *s, const void *K, const void *V, const int32_t *old_lens,
@@ -448,7 +449,9 @@ TLS_API tls_status tls_evict_select(const tls_shape *s, int32_t budget, int32_t 
 /* Moves the kept rows together, in place: row keep_idx[j] of each (sequence,
  * KV head) becomes row j.  Rows from the number of kept ones on are left as
  * they were.  Afterwards the summary and an int8 slab are rebuilt by
- * tls_build_block_meta (a block now holds other tokens).
+ * tls_build_block_meta (a block now holds other tokens).  A 4-bit cache gives
+ * the stored keys for that (tls_kv4_read): its summary then bounds the stored
+ * keys, and the moved label slab still holds the channels of the given ones.
  *   keep_idx   device int32 [B][H_kv][budget], ascending and distinct, -1
  *              padded (tls_evict_select; ids >= max_ctx are ignored)
  *   seq_lens   device int32 [B]: the lengths before the eviction

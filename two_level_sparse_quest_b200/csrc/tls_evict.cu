@@ -23,9 +23,9 @@
 //   it, a chunk for each of its CTAs at a time, so that a single sequence still
 //   fills the GPU.
 // Both are bound by HBM: 4 bytes a token, and each kept row once in and out.
-// Half of 8 x 8 caches of 98304 tokens, K and V in bf16: 569 us in all, the
-// selection 28 of them (the moves 6.0 TB/s); one sequence of 49152 tokens in 4
-// bits 34 us, the selection 15.
+// Half of 8 x 8 caches of 98304 tokens, K and V in bf16: 567 us in all, the
+// selection 28 to 33 of them (by the weights' spread; the moves 6.0 TB/s); one
+// sequence of 49152 tokens in 4 bits 34 us, the selection 12 to 15.
 #include <algorithm>
 
 #include "tls_cache.h"

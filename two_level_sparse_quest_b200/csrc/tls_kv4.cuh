@@ -38,8 +38,9 @@ __device__ __forceinline__ float kv4_scale_value(int b) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(b << 7)));
 }
 
-// x / y for a y whose approximate reciprocal is r: one residual step leaves
-// the quotient within 2^-40, which rounds an exact one (the ties below) exactly.
+// x / y for a y whose approximate reciprocal is r, by one residual correction
+// (q + r (x - q y), P. Markstein, IBM J. Res. Dev. 34, 1990): it leaves the
+// quotient within 2^-40, which rounds an exact one (the ties below) exactly.
 __device__ __forceinline__ float quotient(float x, float y, float r) {
   const float q = x * r;
   return fmaf(fmaf(-q, y, x), r, q);

@@ -10,7 +10,8 @@
 // instructions that widen the codes (two for each pair of channels: e2m1 ->
 // fp16, times the scale, each at half rate) that come near it, not the tensor
 // pipe.  Measured (one B200): 64 groups of 98304 tokens, 4 heads, 174 us (5.2
-// TB/s, 0.80 of the measured copy rate); of 4096 listed ones 19.2 us.
+// TB/s, 0.80 of the measured copy rate), 8 heads 199, 16 heads 338; of 4096
+// listed ones 19.3 us, 8 heads 20.6, 16 heads 29.6.
 //
 // Layout: the tokens are the MMA rows.  S^T[16 tokens x 8 heads] = K q^T takes
 // one m16n8k16 per 16 channels, O^T[16 channels x 8 heads] += V^T P^T one per

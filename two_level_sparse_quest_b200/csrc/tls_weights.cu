@@ -16,9 +16,10 @@
 // queries sit in shared memory as B fragments, in the same order.  fp32 keys
 // take CUDA cores, four lanes a token.
 //
-// Measured (one B200): 64 groups of 4096 listed tokens, 4 heads, bf16 13.8 us
-// (5.1 TB/s), every token of 98304 268 us (6.2 TB/s); the latent's 64 heads over
-// 4 x 2048 tokens 7.1 us, most of it the 73 KB of queries that each SM fetches.
+// Measured (one B200): 64 groups of 4096 listed tokens, 4 heads, bf16 14.0 us
+// (14.8 with inputs past the L2), every token of 98304 267 us (6.2 TB/s), 4-bit
+// keys 11.1 (11.8) and 147 us; the latent's 64 heads over 4 x 2048 tokens 7.1 us
+// (8.6), most of it the 73 KB of queries that each SM fetches, 128 heads 10.4.
 //
 // The exponent is formed as tau s - lse in natural units, rounded once, before
 // it is scaled for exp2: the weights that matter have it near zero.  Each
