@@ -331,8 +331,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_attn_kernel(
     }
     if (vm != 0u && alive) {
       const unsigned char *S = ring + st * L::kStage;
-      // (both halves in one body where the registers allow it: a list's copies leave too few, 19.9 us against 19.7)
-#pragma unroll NT == 1 && !LIST ? 2 : 1
+      // (both halves in one body where the registers allow it: every token 174 us against 179, lists the same)
+#pragma unroll NT == 1 ? 2 : 1
       for (int hf = 0; hf < 2; ++hf, S += R::kBytes) {  // even tokens of the stage, then odd ones
         // ---- S^T = K q^T: rows g, g + 8 of heads 2c, 2c + 1
         float s[NT][4];
